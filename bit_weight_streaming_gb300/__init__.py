@@ -30,6 +30,15 @@ from .api import (  # noqa: F401
     mxfp4_moe_gemv,
     mxfp4_moe_inspect,
 )
+from .serving import (  # noqa: F401
+    KvCache,
+    KvPlan,
+    kv_plan,
+    qk_norm_rope_append,
+    kv_attention,
+    kv_attention_workspace_size,
+    draft_verify,
+)
 
 from . import stack, workloads  # noqa: F401,E402
 

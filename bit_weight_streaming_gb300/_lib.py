@@ -10,6 +10,8 @@ _lib = None
 P = C.c_void_p
 I = C.c_int
 Z = C.c_size_t
+L = C.c_int64
+F = C.c_float
 
 SIGNATURES = {
     "bws_version": (I, []),
@@ -42,6 +44,11 @@ SIGNATURES = {
     "bws_decode_step_kernel_count": (I, [P]),
     "bws_decode_step_tap_size": (Z, [P]),
     "bws_decode_step_tap": (I, [P, P, P, P, Z, P, Z, P]),
+    "bws_kv_plan": (I, [P, P, I, I, P, I, P, P, I, P, P, P, P, P, P, P]),
+    "bws_qk_norm_rope_append": (I, [P, P, P, P]),
+    "bws_kv_attention_workspace_size": (Z, [I, I, I, I]),
+    "bws_kv_attention": (I, [P, L, L, I, I, P, P, I, I, P, P, I, F, P, P, P, Z, P]),
+    "bws_draft_verify": (I, [P, L, P, L, P, I, I, P, I, P, P, I, P, P, P]),
     "bws_status_word": (I, [P, P, P]),
     "bws_debug_wait_flag": (I, [P, C.c_uint32, P, Z, P]),
     "bws_hbm_read_probe": (I, [P, Z, P, P]),
@@ -62,14 +69,14 @@ def lib():
             raise BwsError(
                 f"{LIB_PATH} is missing: build it with "
                 "`python -c 'import __graft_entry__ as g; g.build()'` (needs nvcc)")
-        L = C.CDLL(LIB_PATH)
+        so = C.CDLL(LIB_PATH)
         for name, (res, args) in SIGNATURES.items():
-            f = getattr(L, name, None)
+            f = getattr(so, name, None)
             if f is None:
                 continue
             f.restype = res
             f.argtypes = args
-        _lib = L
+        _lib = so
     return _lib
 
 

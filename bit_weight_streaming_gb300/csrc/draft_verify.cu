@@ -1,0 +1,335 @@
+// Verification of drafted tokens against the target's probabilities, and the
+// token drawn after the last one that stands. Contract in include/bws.h.
+//
+// A request is one cluster of CTAs. Its first warp's lanes test the drafts (a
+// product of two FP32 numbers is exact in FP64, so the test has no rounding);
+// the number that stand picks the row to draw from, whose w = max(p - q, 0) the
+// cluster sums once: every warp owns a contiguous range of the vocabulary and
+// keeps its sum. CTA 0 collects the warps' sums over distributed shared memory,
+// finds the range in which the running sum passes u * total, and reads only
+// that range again (a few hundred words, now in L2) to find the token.
+// A lane adds FP32 numbers in two words (the rounded sum and what the rounding
+// left), which carries 48 bits: on this GPU FP64 adds run at a small fraction
+// of the FP32 rate and would set the time (1.3 FP64 adds per 4-byte word
+// against the HBM rate); FP64 takes over at the warp's 32 sums.
+// Bound: the chain of dependent loads, the cluster's two barriers and the
+// launch for few requests; the bytes of one or two rows a request for many.
+#include <cooperative_groups.h>
+
+#include <atomic>
+
+#include "bws_abi_util.h"
+#include "bws_common.cuh"
+#include "bws_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace bws {
+namespace {
+
+constexpr int kVerifyThreads = 512;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyMaxRows = 32;
+constexpr int kVerifyMaxCluster = 16;
+
+struct VerifyParams {
+  const float* target;
+  long long target_stride;
+  const float* draft;
+  long long draft_stride;
+  const int32_t* tokens;
+  int n_rows, vocab;
+  const int32_t* row_start;
+  const float *accept_u, *sample_u;
+  int max_rows;
+  int32_t *out, *n_out;
+  int vec;   // rows start on 16-byte boundaries
+};
+
+// hi + lo += w, w >= 0
+BWS_DEV void two_word_add(float& hi, float& lo, float w) {
+  const float s = __fadd_rn(hi, w);
+  const float b = __fsub_rn(s, hi);
+  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(w, b)));
+  hi = s;
+}
+
+// The row to draw from: w(v) = max(p - q, 0); q is a row, or certain at token
+// `certain`, or nothing.
+struct Row {
+  const float* p;
+  const float* q;
+  int certain;
+};
+
+BWS_DEV float weight_of(float p, float q) { return fmaxf(__fsub_rn(p, q), 0.0f); }   // NaN gives 0
+
+BWS_DEV float weight_at(const Row& row, int v) {
+  if (v == row.certain) return 0.0f;
+  return weight_of(__ldg(row.p + v), row.q != nullptr ? __ldg(row.q + v) : 0.0f);
+}
+
+BWS_DEV float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+
+// Sum of w over [a, b) by one warp (the same in every lane). a % 4 == 0.
+template <bool VEC, bool HAS_Q>
+BWS_DEV double range_sum(const Row& row, int a, int b, int lane) {
+  float hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+  if constexpr (VEC) {
+    constexpr int U = 4;   // loads in flight: U rows of 512 bytes from p, and from q
+    int v = a + lane * 4;
+    for (; v + (U - 1) * 128 + 3 < b; v += U * 128) {
+      float4 x[U], y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        x[u] = load4(row.p + v + u * 128);
+        if constexpr (HAS_Q) y[u] = load4(row.q + v + u * 128);
+        else y[u] = make_float4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int d = row.certain - (v + u * 128);
+        two_word_add(hi[0], lo[0], d == 0 ? 0.0f : weight_of(x[u].x, y[u].x));
+        two_word_add(hi[1], lo[1], d == 1 ? 0.0f : weight_of(x[u].y, y[u].y));
+        two_word_add(hi[2], lo[2], d == 2 ? 0.0f : weight_of(x[u].z, y[u].z));
+        two_word_add(hi[3], lo[3], d == 3 ? 0.0f : weight_of(x[u].w, y[u].w));
+      }
+    }
+    for (; v < b; v += 128) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (v + k < b) two_word_add(hi[k], lo[k], weight_at(row, v + k));
+    }
+  } else {
+    int v = a + lane;
+    for (; v + 7 * 32 < b; v += 256) {
+      float x[8], y[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        x[u] = __ldg(row.p + v + u * 32);
+        y[u] = HAS_Q ? __ldg(row.q + v + u * 32) : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        two_word_add(hi[u & 3], lo[u & 3], v + u * 32 == row.certain ? 0.0f : weight_of(x[u], y[u]));
+    }
+    for (; v < b; v += 32) two_word_add(hi[0], lo[0], weight_at(row, v));
+  }
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) s += (double)hi[k] + (double)lo[k];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+BWS_DEV double warp_scan(double x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p) {
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ double s_sum[kVerifyWarps];
+  __shared__ int s_stand;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int r = (int)blockIdx.x / n_cta;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int start = min(max(p.row_start[r], 0), p.n_rows);
+  const int rows = min(max(p.row_start[r + 1] - start, 0), min(p.max_rows, p.n_rows - start));
+  if (rows == 0) {   // the whole cluster leaves
+    if (rank == 0) {
+      for (int i = threadIdx.x; i < p.max_rows; i += kVerifyThreads) p.out[(size_t)r * p.max_rows + i] = -1;
+      if (threadIdx.x == 0) p.n_out[r] = 0;
+    }
+    return;
+  }
+  int token = -1;   // lane i of warp 0: draft i
+  if (warp == 0) {
+    bool ok = false;
+    if (lane < rows - 1) {
+      token = p.tokens[start + lane];
+      if (token >= 0 && token < p.vocab) {
+        const float u = p.accept_u[start + lane];
+        const float t = p.target[(start + lane) * p.target_stride + token];
+        const float d = p.draft != nullptr ? p.draft[(start + lane) * p.draft_stride + token] : 1.0f;
+        ok = (double)u * (double)d < (double)t;
+      }
+    }
+    const unsigned b = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) s_stand = b == 0xffffffffu ? 32 : __ffs(~b) - 1;
+  }
+  __syncthreads();
+  const int stand = s_stand;
+  const int here = start + stand;
+  Row row;
+  row.p = p.target + here * p.target_stride;
+  const bool refused = stand < rows - 1;
+  row.q = refused && p.draft != nullptr ? p.draft + here * p.draft_stride : nullptr;
+  row.certain = refused && p.draft == nullptr ? max(p.tokens[here], -1) : -1;
+
+  // a warp's range: a multiple of four words, as even as that allows
+  const int n_warps = n_cta * kVerifyWarps;
+  const int quads = (p.vocab + 3) / 4, per = (quads + n_warps - 1) / n_warps;
+  const int w = rank * kVerifyWarps + warp;
+  auto range_begin = [&](int i) { return (int)min((long long)i * per * 4, (long long)p.vocab); };
+  double total = 0.0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    const int a = range_begin(w), b = range_begin(w + 1);
+    double s;
+    if (p.vec) s = row.q != nullptr ? range_sum<true, true>(row, a, b, lane) : range_sum<true, false>(row, a, b, lane);
+    else s = row.q != nullptr ? range_sum<false, true>(row, a, b, lane) : range_sum<false, false>(row, a, b, lane);
+    if (lane == 0) s_sum[warp] = s;
+    cluster.sync();
+    if (row.q == nullptr && row.certain < 0) break;
+    // Is anything left of the target? Every CTA asks, so that all go on alike.
+    double any = 0.0;
+    for (int i = lane; i < n_warps; i += 32)
+      any = fmax(any, cluster.map_shared_rank(s_sum, i / kVerifyWarps)[i % kVerifyWarps]);
+    if (__any_sync(0xffffffffu, any > 0.0)) break;
+    row.q = nullptr;
+    row.certain = -1;
+    cluster.sync();   // every read of the sums, before they are formed again
+  }
+  if (rank == 0 && warp == 0) {
+    // a lane holds the sums of n_cta * kVerifyWarps / 32 ranges in order
+    const int each = (n_warps + 31) / 32;
+    double mine = 0.0;
+    for (int i = 0; i < each; ++i) {
+      const int k = lane * each + i;
+      if (k < n_warps) mine += cluster.map_shared_rank(s_sum, k / kVerifyWarps)[k % kVerifyWarps];
+    }
+    const double upto = warp_scan(mine, lane);
+    total = __shfl_sync(0xffffffffu, upto, 31);
+    const double t = (double)p.sample_u[r] * total;
+    // the first range whose running sum passes t; else the last that has any
+    double run = upto - mine, before = 0.0, last_before = 0.0;
+    int found = -1, last = -1;
+    for (int i = 0; i < each; ++i) {
+      const int k = lane * each + i;
+      const double s = k < n_warps ? cluster.map_shared_rank(s_sum, k / kVerifyWarps)[k % kVerifyWarps] : 0.0;
+      if (s > 0.0) {
+        last = k;
+        last_before = run;
+        if (found < 0 && run + s > t) { found = k; before = run; }
+      }
+      run += s;
+    }
+    const unsigned fb = __ballot_sync(0xffffffffu, found >= 0), lb = __ballot_sync(0xffffffffu, last >= 0);
+    int k = -1;
+    if (fb != 0u) {
+      const int src = __ffs(fb) - 1;
+      k = __shfl_sync(0xffffffffu, found, src);
+      before = __shfl_sync(0xffffffffu, before, src);
+    } else if (lb != 0u) {
+      const int src = 31 - __clz(lb);
+      k = __shfl_sync(0xffffffffu, last, src);
+      before = __shfl_sync(0xffffffffu, last_before, src);
+    }
+    int drawn = -1;
+    if (k >= 0) {
+      const int a = range_begin(k), b = range_begin(k + 1);
+      double base = before;
+      int fallback = -1;
+      for (int v0 = a; v0 < b && drawn < 0; v0 += 128) {
+        const int v = v0 + lane * 4;
+        float x[4];
+        double own = 0.0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = v + i < b ? weight_at(row, v + i) : 0.0f;
+          own += x[i];
+        }
+        const double scan = warp_scan(own, lane);
+        double at = base + (scan - own);
+        int mine_v = -1, mine_last = -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          at += x[i];
+          if (x[i] > 0.0f) {
+            mine_last = v + i;
+            if (mine_v < 0 && at > t) mine_v = v + i;
+          }
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, mine_v >= 0), any = __ballot_sync(0xffffffffu, mine_last >= 0);
+        if (hit != 0u) drawn = __shfl_sync(0xffffffffu, mine_v, __ffs(hit) - 1);
+        if (any != 0u) fallback = __shfl_sync(0xffffffffu, mine_last, 31 - __clz(any));
+        base += __shfl_sync(0xffffffffu, scan, 31);
+      }
+      if (drawn < 0) drawn = fallback;
+    }
+    if (lane < p.max_rows) {
+      int32_t v = -1;
+      if (lane < stand) v = token;
+      else if (lane == stand) v = drawn;
+      p.out[(size_t)r * p.max_rows + lane] = v;
+    }
+    if (lane == 0) p.n_out[r] = stand + 1;
+  }
+  cluster.sync();   // no CTA leaves while its sums may be read
+}
+
+}  // namespace
+}  // namespace bws
+
+extern "C" int bws_draft_verify(const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
+                                const int32_t* tokens, int n_rows, int vocab, const int32_t* row_start, int n_requests,
+                                const float* accept_u, const float* sample_u, int max_rows, int32_t* out,
+                                int32_t* n_out, void* stream) {
+  using namespace bws;
+  const char* name = "bws_draft_verify";
+  if (n_requests < 0 || n_requests > (1 << 20) || n_rows < 0)
+    return fail(BWS_ERR_INVALID_ARG, "%s: n_requests = %d, n_rows = %d", name, n_requests, n_rows);
+  if (max_rows < 1 || max_rows > kVerifyMaxRows)
+    return fail(BWS_ERR_INVALID_ARG, "%s: max_rows = %d must be in [1, %d]", name, max_rows, kVerifyMaxRows);
+  if (vocab < 1 || vocab > (1 << 28)) return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: vocab = %d", name, vocab);
+  if (n_requests == 0) {
+    clear_error();
+    return BWS_OK;
+  }
+  if (!row_start || !sample_u || !out || !n_out || (n_rows > 0 && (!target || !tokens || !accept_u)))
+    return fail(BWS_ERR_INVALID_ARG, "%s: null pointer", name);
+  if (target_stride < vocab || (draft && draft_stride < vocab))
+    return fail(BWS_ERR_INVALID_ARG, "%s: row strides must be at least the vocabulary", name);
+  const void* ptrs[] = {target, draft, tokens, row_start, accept_u, sample_u, out, n_out};
+  for (const void* q : ptrs)
+    if (!aligned(q, 4)) return fail(BWS_ERR_MISALIGNED, "%s: 4-byte alignment needed", name);
+  VerifyParams p = {target, target_stride, draft, draft_stride, tokens, n_rows, vocab, row_start,
+                    accept_u, sample_u, max_rows, out, n_out, 0};
+  p.vec = aligned(target, 16) && target_stride % 4 == 0 &&
+          (draft == nullptr || (aligned(draft, 16) && draft_stride % 4 == 0));
+  // One request is bound by what an SM can load: as many CTAs as a cluster
+  // takes. Many requests fill the GPU with smaller clusters.
+  int cluster = kVerifyMaxCluster;
+  while (cluster > 1 && (long long)n_requests * cluster > 2LL * num_sms()) cluster >>= 1;
+  // a warp with less than 128 words only adds to the joining
+  while (cluster > 1 && (long long)cluster * kVerifyWarps * 128 > 2LL * vocab) cluster >>= 1;
+  static std::atomic<unsigned long long> attr{0};
+  const unsigned long long bit = 1ull << (current_device() & 63);
+  if (!(attr.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return cuda_status(e, name);
+    attr.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(n_requests * cluster));
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.stream = as_stream(stream);
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = (unsigned)cluster;
+  a[1].val.clusterDim.y = 1;
+  a[1].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 2;
+  return cuda_status(cudaLaunchKernelEx(&cfg, verify_kernel, p), name);
+}

@@ -1,0 +1,829 @@
+// Attention of a step's 1..8 rows per request over the 8-bit cache. Contract in
+// include/bws.h.
+//
+// Mathematics. A kv head's query rows (tokens of the request times the query
+// heads of the group) are the N side of both products, cached tokens and head
+// dimensions the M side: S^T = K Q^T, then O^T = V^T P^T, on m16n8k16 with f16
+// operands and FP32 sums. E4M3 codes are exact in f16. A query row is scaled
+// by a power of two to fit f16 (exact but for values 2^-24 below the row's
+// largest). With a block's scales ks and vs,
+//   x = scale * log2(e) * ks * (q . code) + log2(vs),   w = 2^(x - m),
+//   out = sum w code_v / sum (w / vs),
+// m the running maximum of x: taking the value scale into the exponent keeps
+// every weight in [0, 1], whatever the blocks' scales, so that its rounding to
+// f16 (2^-11, finer than the BF16 result) is relative to the largest term.
+//
+// Work. A segment is one (request, kv head, group of 8 NT rows); its unit is 16
+// cached tokens (one TMA box a side; never across a block). All units of all
+// segments lie on one line that is cut into equal shares, one per CTA, so the
+// CTAs finish together whatever the lengths are; a segment cut by a share's
+// border leaves one partial result (m, l, O) per share in the workspace, which
+// the second kernel joins in share order (no atomics: same bits every run).
+// Lengths are read on the device: every CTA forms the line's prefix itself.
+//
+// Inside a CTA the eight warps are independent: each takes every eighth unit
+// through a ring of its own (TMA boxes, 128-byte swizzle, so that ldmatrix
+// reads without bank conflicts) and keeps its own m, l and O in registers; no
+// barrier joins them before the segment's end.
+// Bound: HBM for few rows; the conversions and mma.sync for many.
+#include <cuda.h>
+#include <string.h>
+
+#include <atomic>
+
+#include "bws_abi_util.h"
+#include "bws_common.cuh"
+#include "bws_internal.h"
+#include "kv_cache.cuh"
+#include "stream_tile.cuh"
+
+namespace bws {
+namespace {
+
+constexpr int kAttnWarps = 8;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kUnit = 16;                  // cached tokens of a unit
+constexpr int kAttnMaxRows = kMaxTokens;   // rows of a request
+constexpr int kAttnMaxGroup = 16;          // query heads of a kv head
+constexpr uint32_t kAttnPolls = 1u << 22;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnParams {
+  CUtensorMap k, v;
+  const uint16_t* q;
+  long long q_row_stride, q_head_stride;
+  int n_rows, H, K, G;
+  int B, n_blocks;
+  const float *k_scale, *v_scale;
+  const int32_t* table;
+  int max_blocks, R;
+  const int32_t *row_start, *kv_lens;
+  int max_rows;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  float* part_o;      // [2 * CTAs][8 NT][D]
+  float2* part_ml;    // [2 * CTAs][8 NT]
+  uint32_t* failed;   // [CTAs]
+  uint32_t* hdr;
+  int n_ctas, least;  // CTAs; smallest share in units
+};
+
+// ---- the line of units -----------------------------------------------------------
+
+struct Request {
+  int rows, start, kv, units, groups;   // kv: cached tokens; units of one segment; row groups
+};
+
+BWS_DEV Request request_of(const AttnParams& p, int r, int group_rows) {
+  Request q;
+  q.start = min(max(p.row_start[r], 0), p.n_rows);
+  q.rows = min(max(p.row_start[r + 1] - q.start, 0), min(p.max_rows, p.n_rows - q.start));
+  const long long cap = (long long)p.max_blocks * p.B;
+  q.kv = (int)min((long long)max(p.kv_lens[r], 0), cap);
+  q.units = max(1, (q.kv + kUnit - 1) / kUnit);   // a request without tokens still writes its rows
+  q.groups = (q.rows * p.G + group_rows - 1) / group_rows;
+  return q;
+}
+
+BWS_DEV long long units_of(const AttnParams& p, const Request& q) { return (long long)p.K * q.groups * q.units; }
+
+struct Line {
+  long long total, share;
+  int r;            // request that holds the asked unit
+  long long base;   // its first unit
+};
+
+// The whole CTA: total units, share, and the request of unit pick(share)
+// (clamped to the line).
+template <class Pick>
+BWS_DEV Line find_on_line(const AttnParams& p, int group_rows, Pick pick, long long* s_warp, long long* s_found) {
+  const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.R + n - 1) / n;
+  const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += units_of(p, request_of(p, r, group_rows));
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += a;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  long long before = inc - mine, total = 0;
+  for (int w = 0; w < n / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  Line line;
+  line.total = total;
+  long long share = (total + p.n_ctas - 1) / p.n_ctas;
+  line.share = share < p.least ? p.least : share;
+  const long long u = pick(line.share);
+  if (u >= before && u < before + mine) {
+    long long b = before;
+    int r = r0;
+    for (; r < r1 - 1; ++r) {
+      const long long k = units_of(p, request_of(p, r, group_rows));
+      if (u < b + k) break;
+      b += k;
+    }
+    s_found[0] = r;
+    s_found[1] = b;
+  }
+  __syncthreads();
+  line.r = (int)s_found[0];
+  line.base = s_found[1];
+  return line;
+}
+
+// ---- tiles ---------------------------------------------------------------------
+
+BWS_DEV void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w, uint32_t bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;"
+      :: "r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(pol) : "memory");
+}
+BWS_DEV void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+BWS_DEV void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+BWS_DEV uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+BWS_DEV uint2 lds_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+BWS_DEV float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+BWS_DEV void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <int D, int NT>
+struct Shape {
+  static constexpr int kRowBytes = D < 128 ? D : 128;         // bytes of a swizzled row
+  static constexpr int kPanels = D / kRowBytes;               // panels of 16 tokens x kRowBytes
+  static constexpr int kSide = kUnit * D;                     // bytes of a unit's keys, or values
+  static constexpr int kStage = 2 * kSide;
+  // A ring at least as deep as a warp's O in FP32 (the segment's end reuses
+  // it), three stages or 12 KB at the least: two CTAs an SM then keep 96 KB or
+  // more in flight, well above the 36 KB that HBM's latency asks of an SM.
+  static constexpr int kStages = NT > 3 ? (D == 64 && NT < 6 ? 6 : NT) : (D == 64 ? 6 : 3);
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kRows = 8 * NT;
+  static constexpr bool kQInRegs = NT * D <= 256;
+  static constexpr int kQStride = 2 * D + 16;                 // bytes of a query row, off the banks' period
+};
+
+template <int D, int NT>
+struct __align__(16) Tail {
+  uint8_t q[8 * NT * Shape<D, NT>::kQStride];
+  float q_scale[8 * NT];
+  float m[kAttnWarps][8 * NT];
+  float l[kAttnWarps][8 * NT];
+  uint32_t nan_mask[D];                                       // bit j: token j of the rows' own has a NaN there
+  float2 scales[kAttnWarps][Shape<D, NT>::kStages];           // ks, vs; ks = -1: the block is not there
+  unsigned long long full[kAttnWarps][Shape<D, NT>::kStages];
+  long long line_warp[kAttnWarps];
+  long long line_found[2];
+  uint32_t failed;
+};
+
+// Byte offset of 16-byte chunk `c` of token row `row` in a side.
+template <int D>
+BWS_DEV uint32_t chunk_at(int row, int c) {
+  if constexpr (D == 64) return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+  else return (c >> 3) * (kUnit * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kRing * kAttnWarps <= 100 * 1024 ? 2 : 1)
+attn_kernel(const __grid_constant__ AttnParams p) {
+  using S = Shape<D, NT>;
+  constexpr int kMT = D / 16;   // m tiles of O^T
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  Tail<D, NT>& T = *reinterpret_cast<Tail<D, NT>*>(smem_raw + (base - smem_u32(smem_raw)) + S::kRing * kAttnWarps);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t4 = lane & 3;
+  const uint32_t ring = base + warp * S::kRing;
+  const uint32_t bar0 = smem_u32(&T.full[warp][0]);
+  if (lane == 0) {
+    for (int s = 0; s < S::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
+    mbar_fence_init();
+  }
+  if (tid == 0) T.failed = 0;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int cta = blockIdx.x;
+  const Line line = find_on_line(p, S::kRows, [&](long long share) { return cta * share; }, T.line_warp, T.line_found);
+  const long long u0 = cta * line.share, u1 = min(line.total, u0 + line.share);
+  const uint64_t pol = l2_evict_first();
+  uint32_t phase_base = 0;   // units this warp has put through its ring
+  bool dead = false;
+  // this lane's ldmatrix row: tokens 0-7 and 8-15 of one chunk, then of the next
+  const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lchunk = lane >> 4;
+
+  int r = line.r;
+  long long rbase = line.base;
+  long long u = u0;
+  while (u < u1) {
+    const Request rq = request_of(p, r, S::kRows);
+    const long long rn = units_of(p, rq);
+    if (u >= rbase + rn) {   // on to the next request
+      rbase += rn;
+      ++r;
+      continue;
+    }
+    const int seg = (int)((u - rbase) / rq.units);
+    const long long seg_a = rbase + (long long)seg * rq.units, seg_b = seg_a + rq.units;
+    const int head = seg / rq.groups, row0 = (seg % rq.groups) * S::kRows;
+    const int first = (int)(u - seg_a), last = (int)(min(u1, seg_b) - seg_a);   // units [first, last)
+    const int n_group_rows = min(rq.rows * p.G - row0, S::kRows);
+    const int seen0 = rq.kv - rq.rows;   // row j sees tokens <= seen0 + j
+    // ---- this warp's units: first + warp, + 8, ...
+    const int mine = (last - first - warp + kAttnWarps - 1) / kAttnWarps;
+    const int32_t* table = p.table + (size_t)r * p.max_blocks;
+    // Blocks of 32 of the warp's units at a time, one a lane.
+    int ids = 0;
+    float ks_l = 0.0f, vs_l = 0.0f;
+    auto look_up = [&](int i0) {
+      const int i = i0 + lane;
+      ids = -1;
+      if (i < mine) {
+        const int tok = (first + warp + i * kAttnWarps) * kUnit;
+        if (tok < rq.kv) {
+          const int b = table[tok / p.B];
+          if (b >= 0 && b < p.n_blocks) {
+            ids = b;
+            ks_l = p.k_scale[(size_t)b * p.K + head];
+            vs_l = p.v_scale[(size_t)b * p.K + head];
+          }
+        }
+      }
+    };
+    auto issue = [&](int i) {   // the whole warp; unit i of this warp into its stage
+      if ((i & 31) == 0) look_up(i);
+      const int b = __shfl_sync(0xffffffffu, ids, i & 31);
+      const float ks = __shfl_sync(0xffffffffu, ks_l, i & 31), vs = __shfl_sync(0xffffffffu, vs_l, i & 31);
+      const int s = (int)((phase_base + i) % S::kStages);
+      if (lane == 0) {
+        T.scales[warp][s] = b >= 0 ? make_float2(ks, vs) : make_float2(-1.0f, 0.0f);
+        const uint32_t bar = bar0 + 8 * s, dst = ring + s * S::kStage;
+        if (b >= 0) {
+          mbar_arrive_expect_tx(bar, S::kStage);
+          const int tok = ((first + warp + i * kAttnWarps) * kUnit) % p.B;
+#pragma unroll
+          for (int x = 0; x < S::kPanels; ++x) {
+            tma_load_4d(dst + x * kUnit * 128, &p.k, x * 128, tok, head, b, bar, pol);
+            tma_load_4d(dst + S::kSide + x * kUnit * 128, &p.v, x * 128, tok, head, b, bar, pol);
+          }
+        } else {
+          mbar_arrive(bar);
+        }
+      }
+      __syncwarp();
+    };
+    const int ahead = min(mine, S::kStages);
+    if (!dead)
+      for (int i = 0; i < ahead; ++i) issue(i);
+
+    // ---- queries to f16, a warp a row
+    for (int n = warp; n < S::kRows; n += kAttnWarps) {
+      uint16_t* dst = reinterpret_cast<uint16_t*>(T.q + n * S::kQStride);
+      float x[D / 32];
+      float top = 0.0f;
+      if (n < n_group_rows) {
+        const int j = (row0 + n) / p.G, h = head * p.G + (row0 + n) % p.G;
+        const uint16_t* src = p.q + (rq.start + j) * p.q_row_stride + h * p.q_head_stride;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          x[i] = __uint_as_float((uint32_t)src[lane + 32 * i] << 16);
+          if (fabsf(x[i]) < INFINITY) top = fmaxf(top, fabsf(x[i]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) x[i] = 0.0f;
+      }
+      top = warp_max(top);
+      const int e = top > 0.0f ? min(max(floor_log2_abs(top), -100), 126) : 0;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        dst[lane + 32 * i] = __half_as_ushort(__float2half_rn(ldexp_exact(x[i], -e)));
+      if (lane == 0) T.q_scale[n] = p.scale * kLog2e * exp2i(e);
+    }
+    for (int i = tid; i < D; i += kAttnThreads) T.nan_mask[i] = 0;
+    __syncthreads();
+
+    uint32_t qf[S::kQInRegs ? kMT : 1][S::kQInRegs ? NT : 1][2];
+    const uint32_t q_at = smem_u32(T.q) + g * S::kQStride + t4 * 8;
+    if constexpr (S::kQInRegs) {
+#pragma unroll
+      for (int c = 0; c < kMT; ++c)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint2 b = lds_v2(q_at + n * 8 * S::kQStride + c * 32);
+          qf[c][n][0] = b.x;
+          qf[c][n][1] = b.y;
+        }
+    }
+    float qs[NT][2], m[NT][2], l[NT][2];
+    float o[kMT][NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        qs[n][k] = T.q_scale[n * 8 + t4 * 2 + k];
+        m[n][k] = -INFINITY;
+        l[n][k] = 0.0f;
+      }
+#pragma unroll
+    for (int c = 0; c < kMT; ++c)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[c][n][k] = 0.0f;
+
+    for (int i = 0; i < mine; ++i) {
+      const uint32_t it = phase_base + i;
+      const int s = (int)(it % S::kStages);
+      const uint32_t ks_at = ring + s * S::kStage, vs_at = ks_at + S::kSide;
+      if (!dead && !mbar_wait_bounded(bar0 + 8 * s, (it / S::kStages) & 1, kAttnPolls)) dead = true;
+      if (__any_sync(0xffffffffu, dead)) {
+        dead = true;
+        if (lane == 0) T.failed = 1;
+        for (int k = i + 1; k < min(i + S::kStages, mine); ++k) {   // the copies still on their way
+          const uint32_t at = phase_base + k;
+          mbar_wait_bounded(bar0 + 8 * (at % S::kStages), (at / S::kStages) & 1, kAttnPolls);
+        }
+        break;
+      }
+      const float2 sc = T.scales[warp][s];
+      const int tok0 = (first + warp + i * kAttnWarps) * kUnit;
+      if (sc.x != -1.0f) {
+        const float vs = fminf(fmaxf(sc.y, 0x1p-60f), 0x1p60f);
+        const float lvs = log2f(vs), rvs = 1.0f / vs;
+        // ---- S^T: 16 tokens x rows
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[n][k] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kMT; c += 2) {
+          uint32_t w[4];
+          ldsm_x4(ks_at + chunk_at<D>(lrow, c + lchunk), w);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x2x2(w[2 * h], a0, a2);
+            e4m3x4_to_f16x2x2(w[2 * h + 1], a1, a3);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              uint32_t b0, b1;
+              if constexpr (S::kQInRegs) {
+                b0 = qf[c + h][n][0];
+                b1 = qf[c + h][n][1];
+              } else {
+                const uint2 b = lds_v2(q_at + n * 8 * S::kQStride + (c + h) * 32);
+                b0 = b.x;
+                b1 = b.y;
+              }
+              mma_f16_16816(acc[n], a0, a1, a2, a3, b0, b1);
+            }
+          }
+        }
+        // ---- exponents, masks
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[n][k] = fmaf(acc[n][k], sc.x * qs[n][k & 1], lvs);
+        if (tok0 + kUnit - 1 > seen0) {   // the end: some rows do not see all 16
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int lim = min(seen0 + (row0 + n * 8 + t4 * 2 + k) / p.G, rq.kv - 1);
+              if (tok0 + g > lim) acc[n][k] = -INFINITY;
+              if (tok0 + g + 8 > lim) acc[n][k + 2] = -INFINITY;
+            }
+          // Values no row or not every row may see: rows past the end are
+          // zeroed (their memory may hold anything), and a NaN among the rows'
+          // own tokens is taken out here and put back at the end for the rows
+          // that do see it; 0 * NaN would reach the others.
+          __syncwarp();
+          for (int b = lane; b < kUnit * (D / 4); b += 32) {
+            const int tk = b / (D / 4), byte = (b % (D / 4)) * 4, own = tok0 + tk - seen0;
+            if (own <= 0) continue;
+            const uint32_t at = vs_at + chunk_at<D>(tk, byte >> 4) + (byte & 15);
+            uint32_t x;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at));
+            if (tok0 + tk >= rq.kv) {
+              x = 0;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (((x >> (8 * k)) & 0x7Fu) == 0x7Fu) {
+                  x &= ~(0xFFu << (8 * k));
+                  atomicOr(&T.nan_mask[byte + k], 1u << own);
+                }
+            }
+            asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(x) : "memory");
+          }
+          proxy_fence();   // before TMA writes the stage again
+          __syncwarp();
+        }
+        // ---- running maximum
+        float mn[NT][2];
+        bool grew = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float v = fmaxf(acc[n][k], acc[n][k + 2]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
+            mn[n][k] = fmaxf(m[n][k], v);
+            grew |= mn[n][k] > m[n][k];
+          }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float f = mn[n][k] == -INFINITY ? 1.0f : exp2_fast(m[n][k] - mn[n][k]);
+              m[n][k] = mn[n][k];
+              l[n][k] *= f;
+#pragma unroll
+              for (int c = 0; c < kMT; ++c) {
+                o[c][n][k] *= f;
+                o[c][n][k + 2] *= f;
+              }
+            }
+        }
+        // ---- weights, their sums, P^T as the second product's B operand
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float wv[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float mm = m[n][k & 1];
+            wv[k] = exp2_fast(acc[n][k] - (mm == -INFINITY ? 0.0f : mm));
+          }
+          l[n][0] = fmaf(wv[0] + wv[2], rvs, l[n][0]);
+          l[n][1] = fmaf(wv[1] + wv[3], rvs, l[n][1]);
+          const __half2 h0 = __floats2half2_rn(wv[0], wv[1]), h1 = __floats2half2_rn(wv[2], wv[3]);
+          pb[n][0] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h0));
+          pb[n][1] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h1));
+        }
+        // ---- O^T += V^T P^T; m row g is dimension 2 g of the chunk, g + 8 is 2 g + 1
+#pragma unroll
+        for (int c = 0; c < kMT; c += 2) {
+          uint32_t w[4];
+          ldsm_x4_t(vs_at + chunk_at<D>(lrow, c + lchunk), w);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x2x2(__byte_perm(w[2 * h], 0, 0x3120), a0, a1);
+            e4m3x4_to_f16x2x2(__byte_perm(w[2 * h + 1], 0, 0x3120), a2, a3);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16_16816(o[c + h][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (i + S::kStages < mine) issue(i + S::kStages);
+    }
+    phase_base += max(mine, 0);
+
+    // ---- the segment's end: join the warps' m, l, O
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], x);
+        if (g == 0) {
+          T.m[warp][n * 8 + t4 * 2 + k] = m[n][k];
+          T.l[warp][n * 8 + t4 * 2 + k] = l[n][k];
+        }
+      }
+    float* mine_o = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw))) + warp * (S::kRing / 4);
+    if (mine > 0) {
+#pragma unroll
+      for (int c = 0; c < kMT; ++c)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float2*>(mine_o + (n * 8 + t4 * 2 + k) * D + c * 16 + 2 * g) =
+                make_float2(o[c][n][k], o[c][n][k + 2]);
+    }
+    __syncthreads();
+    const bool whole = seg_a >= u0 && seg_b <= u1;
+    const int slot = cta * 2 + (seg_a <= u0 ? 0 : 1);
+    const int n_live = min(last - first, kAttnWarps);   // warps that had a unit
+    for (int e = tid; e < n_group_rows * (D / 4); e += kAttnThreads) {
+      const int n = e / (D / 4), d = (e % (D / 4)) * 4;
+      float top = -INFINITY;
+      for (int w = 0; w < n_live; ++w) top = fmaxf(top, T.m[w][n]);
+      float sum = 0.0f;
+      float4 a = make_float4(0, 0, 0, 0);
+      for (int w = 0; w < n_live; ++w) {
+        const float mw = T.m[w][n];
+        // a warp whose every weight is NaN still has m = -inf and must show
+        const float f = mw == top ? 1.0f : exp2_fast(mw - top);
+        const float4 b = *reinterpret_cast<const float4*>(
+            reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw))) + w * (S::kRing / 4) + n * D + d);
+        sum = fmaf(T.l[w][n], f, sum);
+        a.x = fmaf(b.x, f, a.x);
+        a.y = fmaf(b.y, f, a.y);
+        a.z = fmaf(b.z, f, a.z);
+        a.w = fmaf(b.w, f, a.w);
+      }
+      const int j = (row0 + n) / p.G, h = head * p.G + (row0 + n) % p.G;
+      const uint32_t see = (2u << j) - 1u;
+      if (T.nan_mask[d] & see) a.x = NAN;
+      if (T.nan_mask[d + 1] & see) a.y = NAN;
+      if (T.nan_mask[d + 2] & see) a.z = NAN;
+      if (T.nan_mask[d + 3] & see) a.w = NAN;
+      if (whole) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+        const size_t at = (size_t)(rq.start + j) * p.H + h;
+        *reinterpret_cast<uint2*>(p.out + at * D + d) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+        if (p.lse != nullptr && d == 0) p.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * S::kRows + n) * D + d) = a;
+        if (d == 0) p.part_ml[(size_t)slot * S::kRows + n] = make_float2(top, sum);
+      }
+    }
+    proxy_fence();   // O lay where TMA writes next
+    __syncthreads();
+    u = seg_a + last;
+  }
+  __syncthreads();
+  if (tid == 0) p.failed[cta] = T.failed;
+}
+
+// Joins the partial results of the segment that share x starts and does not
+// end; one row a CTA of the y axis, one float a thread.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kRows = 8 * NT;
+  constexpr int kLanes = D / 4;            // threads of a row
+  constexpr int kPer = 256 / kLanes;       // pieces read side by side
+  __shared__ long long s_warp[8], s_found[2];
+  __shared__ float4 s_a[kPer][kLanes];
+  __shared__ float s_l[kPer];
+  __shared__ uint32_t s_bad;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int c = blockIdx.x;
+  if (c == 0 && blockIdx.y == 0) {
+    if (threadIdx.x == 0) s_bad = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.n_ctas; i += 256)
+      if (p.failed[i] != 0) s_bad = 1;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      p.hdr[0] = 0;
+      p.hdr[1] = s_bad ? (uint32_t)BWS_STATUS_WAIT_TIMEOUT : 0u;
+    }
+  }
+  const Line line = find_on_line(p, kRows, [&](long long share) { return (c + 1) * share - 1; }, s_warp, s_found);
+  const long long u1 = (c + 1) * line.share;
+  if (u1 >= line.total) return;   // the last share: its segment ends in it
+  const Request rq = request_of(p, line.r, kRows);
+  const int seg = (int)((u1 - 1 - line.base) / rq.units);
+  const long long seg_a = line.base + (long long)seg * rq.units, seg_b = seg_a + rq.units;
+  if (seg_a < u1 - line.share || seg_b <= u1) return;   // begins earlier, or ends here
+  const int pieces = (int)((seg_b - 1) / line.share) - c + 1;
+  const int head = seg / rq.groups, row0 = (seg % rq.groups) * kRows;
+  const int n = blockIdx.y;
+  if (n >= min(rq.rows * p.G - row0, kRows)) return;
+  const int slot0 = c * 2 + (seg_a <= u1 - line.share ? 0 : 1);
+  auto slot_of = [&](int i) { return i == 0 ? slot0 : (c + i) * 2; };
+  const int d4 = threadIdx.x % kLanes, at = threadIdx.x / kLanes;
+  float top = -INFINITY;
+  for (int i = 0; i < pieces; ++i) top = fmaxf(top, p.part_ml[(size_t)slot_of(i) * kRows + n].x);
+  float4 a = make_float4(0, 0, 0, 0);
+  float l = 0.0f;
+#pragma unroll 4
+  for (int i = at; i < pieces; i += kPer) {
+    const size_t row = (size_t)slot_of(i) * kRows + n;
+    const float2 ml = p.part_ml[row];
+    const float4 b = reinterpret_cast<const float4*>(p.part_o + row * D)[d4];
+    const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
+    l = fmaf(ml.y, f, l);
+    a.x = fmaf(b.x, f, a.x);
+    a.y = fmaf(b.y, f, a.y);
+    a.z = fmaf(b.z, f, a.z);
+    a.w = fmaf(b.w, f, a.w);
+  }
+  s_a[at][d4] = a;
+  if (d4 == 0) s_l[at] = l;
+  __syncthreads();
+  if (at != 0) return;
+#pragma unroll
+  for (int i = 1; i < kPer; ++i) {
+    const float4 b = s_a[i][d4];
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+    l += s_l[i];
+  }
+  const int j = (row0 + n) / p.G, h = head * p.G + (row0 + n) % p.G;
+  const size_t o = (size_t)(rq.start + j) * p.H + h;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+  reinterpret_cast<uint2*>(p.out + o * D)[d4] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  if (p.lse != nullptr && d4 == 0) p.lse[o] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+}
+
+// ---- host ------------------------------------------------------------------------
+
+// n8 tiles of a row group: the rows of a full request, rounded up to a form
+// that is built; more rows than fit the registers (NT * D <= 512) go in several
+// groups, each of which reads the cache again.
+int tiles_for(int D, int rows) {
+  const int most = 512 / D, want = (rows + 7) / 8;
+  int nt = 1;
+  while (nt < want && nt < most) nt *= 2;
+  return nt;
+}
+
+template <int D, int NT>
+constexpr int attn_smem() { return Shape<D, NT>::kRing * kAttnWarps + (int)sizeof(Tail<D, NT>) + 1024; }
+
+int ctas_per_sm(int D, int nt) {
+  const int ring = (nt > 3 ? (D == 64 && nt < 6 ? 6 : nt) : (D == 64 ? 6 : 3)) * 2 * kUnit * D * kAttnWarps;
+  return ring <= 100 * 1024 ? 2 : 1;
+}
+
+struct AttnLayout {
+  size_t off_failed, off_ml, off_o, total;
+  int n_ctas, nt;
+};
+
+AttnLayout attn_layout(int H, int K, int D, int max_rows) {
+  AttnLayout L;
+  L.nt = tiles_for(D, max_rows * (H / K));
+  L.n_ctas = num_sms() * ctas_per_sm(D, L.nt);
+  const size_t rows = (size_t)2 * L.n_ctas * 8 * L.nt;
+  // bws_status_word reads 8 bytes here and eight words from 512 on
+  size_t o = 1024;
+  L.off_failed = o; o += align256(sizeof(uint32_t) * (size_t)L.n_ctas);
+  L.off_ml = o; o += align256(sizeof(float2) * rows);
+  L.off_o = o; o += align256(sizeof(float) * rows * D);
+  L.total = o;
+  return L;
+}
+
+bool attn_dims_ok(int H, int K, int D, int max_rows) {
+  return (D == 64 || D == 128 || D == 256) && K >= 1 && K <= 128 && H >= K && H % K == 0 && H / K <= kAttnMaxGroup &&
+         max_rows >= 1 && max_rows <= kAttnMaxRows;
+}
+
+template <int D, int NT>
+cudaError_t launch_attn(const AttnParams& p, cudaStream_t st) {
+  static std::atomic<unsigned long long> attr{0};
+  cudaError_t e = set_smem_once(attr, attn_kernel<D, NT>, attn_smem<D, NT>());
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.n_ctas);
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = attn_smem<D, NT>();
+  cfg.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn_kernel<D, NT>, p);
+  if (e != cudaSuccess) return e;
+  const int rows = p.max_rows * p.G;
+  cfg.gridDim = dim3((unsigned)p.n_ctas, (unsigned)(rows < 8 * NT ? rows : 8 * NT));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, p);
+}
+
+template <int D>
+cudaError_t launch_attn_d(int nt, const AttnParams& p, cudaStream_t st) {
+  if (nt == 1) return launch_attn<D, 1>(p, st);
+  if (nt == 2) return launch_attn<D, 2>(p, st);
+  if constexpr (D <= 128) {
+    if (nt == 4) return launch_attn<D, 4>(p, st);
+  }
+  if constexpr (D <= 64) {
+    if (nt == 8) return launch_attn<D, 8>(p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+}  // namespace bws
+
+extern "C" {
+
+size_t bws_kv_attention_workspace_size(int n_q_heads, int n_kv_heads, int head_dim, int max_rows) {
+  using namespace bws;
+  if (!attn_dims_ok(n_q_heads, n_kv_heads, head_dim, max_rows)) return 0;
+  return attn_layout(n_q_heads, n_kv_heads, head_dim, max_rows).total;
+}
+
+int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int n_rows, int n_q_heads,
+                     const bws_kv_cache* cache, const int32_t* block_table, int max_blocks, int n_requests,
+                     const int32_t* row_start, const int32_t* kv_lens, int max_rows, float scale, uint16_t* out,
+                     float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace bws;
+  const char* name = "bws_kv_attention";
+  const int rc = check_kv_cache(cache, name);
+  if (rc) return rc;
+  const int D = cache->head_dim, K = cache->n_kv_heads;
+  if (max_rows < 1 || max_rows > kAttnMaxRows)
+    return fail(BWS_ERR_INVALID_ARG, "%s: max_rows = %d must be in [1, %d]", name, max_rows, kAttnMaxRows);
+  if (!attn_dims_ok(n_q_heads, K, D, max_rows))
+    return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: n_q_heads = %d must be 1 to %d times n_kv_heads = %d", name, n_q_heads,
+                kAttnMaxGroup, K);
+  if (n_rows < 0 || n_requests < 0 || n_requests > (1 << 20) || max_blocks < 0)
+    return fail(BWS_ERR_INVALID_ARG, "%s: n_rows = %d, n_requests = %d, max_blocks = %d", name, n_rows, n_requests,
+                max_blocks);
+  if ((long long)max_blocks * cache->block_tokens >= (1LL << 31))
+    return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: a table row of %d blocks passes 2^31 tokens", name, max_blocks);
+  if (n_rows == 0 || n_requests == 0) {
+    clear_error();
+    return BWS_OK;
+  }
+  if (!q || !out || !row_start || !kv_lens || (max_blocks > 0 && !block_table))
+    return fail(BWS_ERR_INVALID_ARG, "%s: null pointer", name);
+  if (!(scale > -INFINITY && scale < INFINITY)) return fail(BWS_ERR_INVALID_ARG, "%s: scale must be finite", name);
+  if (!aligned(q, 16) || !aligned(out, 16) || q_row_stride % 8 || q_head_stride % 8 || !aligned(block_table, 4) ||
+      !aligned(row_start, 4) || !aligned(kv_lens, 4) || !aligned(lse, 4))
+    return fail(BWS_ERR_MISALIGNED, "%s: q and out 16-byte, strides of 8 elements, other pointers 4-byte needed", name);
+  const AttnLayout L = attn_layout(n_q_heads, K, D, max_rows);
+  if (!workspace || workspace_bytes < L.total)
+    return fail(BWS_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", name, L.total, workspace_bytes);
+  if (!aligned(workspace, 256)) return fail(BWS_ERR_MISALIGNED, "%s: workspace must be 256-byte aligned", name);
+  if (!tensor_maps_available()) return fail(BWS_ERR_CUDA, "%s: the driver's tensor-map encoder is unavailable", name);
+  char* w = static_cast<char*>(workspace);
+  AttnParams p;
+  memset(&p, 0, sizeof(p));
+  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)cache->block_tokens, (uint64_t)K, (uint64_t)cache->n_blocks};
+  const uint64_t strides[3] = {(uint64_t)D, cache->head_stride, cache->block_stride};
+  if (!encode_4d(&p.k, cache->k, dims, strides, D < 128 ? D : 128, kUnit) ||
+      !encode_4d(&p.v, cache->v, dims, strides, D < 128 ? D : 128, kUnit))
+    return fail(BWS_ERR_CUDA, "%s: tensor map encoding failed", name);
+  p.q = q;
+  p.q_row_stride = q_row_stride;
+  p.q_head_stride = q_head_stride;
+  p.n_rows = n_rows;
+  p.H = n_q_heads;
+  p.K = K;
+  p.G = n_q_heads / K;
+  p.B = cache->block_tokens;
+  p.n_blocks = cache->n_blocks;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.table = block_table;
+  p.max_blocks = max_blocks;
+  p.R = n_requests;
+  p.row_start = row_start;
+  p.kv_lens = kv_lens;
+  p.max_rows = max_rows;
+  p.scale = scale;
+  p.out = out;
+  p.lse = lse;
+  p.hdr = reinterpret_cast<uint32_t*>(w);
+  p.failed = reinterpret_cast<uint32_t*>(w + L.off_failed);
+  p.part_ml = reinterpret_cast<float2*>(w + L.off_ml);
+  p.part_o = reinterpret_cast<float*>(w + L.off_o);
+  p.n_ctas = L.n_ctas;
+  p.least = kAttnWarps;   // a unit for every warp
+  cudaStream_t st = as_stream(stream);
+  cudaError_t e;
+  if (D == 64) e = launch_attn_d<64>(L.nt, p, st);
+  else if (D == 128) e = launch_attn_d<128>(L.nt, p, st);
+  else e = launch_attn_d<256>(L.nt, p, st);
+  return cuda_status(e, name);
+}
+
+}  // extern "C"

@@ -1,0 +1,560 @@
+// The 8-bit key/value cache: block tables and slots from request lengths, and
+// the norm, rotation and E4M3 write of a step's queries, keys and values.
+// Contracts in include/bws.h.
+#include "bws_abi_util.h"
+#include "bws_common.cuh"
+#include "bws_internal.h"
+#include "kv_cache.cuh"
+
+namespace bws {
+namespace {
+
+// ---- block tables and slots -----------------------------------------------------
+//
+// Everything follows from two running sums over the requests: rows before a
+// request and blocks taken before it. Every CTA forms both sums for all
+// requests itself (two loads a request, shared by L2) and then fills its share
+// of the rows and of the taken blocks, so one launch suffices and no CTA waits
+// for another. A row inside a block that this call takes reads it from the
+// free list, not from the table entry another CTA is writing.
+// Bound: launch and the chain of two dependent loads for few requests, the 8
+// bytes written per row for many.
+
+constexpr int kPlanThreads = 256;
+constexpr int kPlanMaxRequests = 4096;
+
+struct PlanParams {
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int R, B;
+  int32_t* table;
+  int max_blocks;
+  const int32_t* free_blocks;
+  const int32_t* n_free;
+  int n_rows;
+  int32_t *slots, *positions, *row_start, *kv_lens, *n_free_out, *status;
+};
+
+// Largest r in [0, n) with a[r] <= i, a non-decreasing and a[0] = 0.
+BWS_DEV int last_not_above(const int* a, int n, int i) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+BWS_DEV int clamp_i32(long long v) { return v > 0x7fffffffLL ? 0x7fffffff : (int)v; }
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
+  extern __shared__ int s_plan[];   // rows before [R + 1], then blocks before [R + 1]
+  int* s_row = s_plan;
+  int* s_blk = s_plan + p.R + 1;
+  __shared__ long long s_wr[kPlanThreads / 32], s_wb[kPlanThreads / 32];
+  __shared__ int s_over;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (tid == 0) s_over = 0;
+  const int n_free = max(*p.n_free, 0);
+  const int per = (p.R + kPlanThreads - 1) / kPlanThreads;
+  const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
+  long long rows = 0, blks = 0;
+  bool over = false;
+  for (int r = r0; r < r1; ++r) {
+    const long long seq = max(p.seq_lens[r], 0), nw = max(p.new_lens[r], 0);
+    const long long have = (seq + p.B - 1) / p.B, need = (seq + nw + p.B - 1) / p.B;
+    s_row[r] = (int)nw;
+    s_blk[r] = (int)(need - have);
+    rows += nw;
+    blks += need - have;
+    over |= need > p.max_blocks;
+  }
+  long long ir = rows, ib = blks;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, ir, o), b = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) { ir += a; ib += b; }
+  }
+  if (lane == 31) { s_wr[warp] = ir; s_wb[warp] = ib; }
+  __syncthreads();
+  if (over) s_over = 1;
+  long long br = ir - rows, bb = ib - blks, tr = 0, tb = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) { br += s_wr[w]; bb += s_wb[w]; }
+    tr += s_wr[w];
+    tb += s_wb[w];
+  }
+  for (int r = r0; r < r1; ++r) {   // sums past 2^31 - 1 saturate: rows and free blocks end far below
+    const int nr = s_row[r], nb = s_blk[r];
+    s_row[r] = clamp_i32(br);
+    s_blk[r] = clamp_i32(bb);
+    br += nr;
+    bb += nb;
+  }
+  if (tid == 0) { s_row[p.R] = clamp_i32(tr); s_blk[p.R] = clamp_i32(tb); }
+  __syncthreads();
+  const int total = s_row[p.R], taken = s_blk[p.R];
+  if (blockIdx.x == 0) {
+    for (int r = tid; r <= p.R; r += kPlanThreads) {
+      p.row_start[r] = s_row[r];
+      if (r < p.R) p.kv_lens[r] = clamp_i32((long long)max(p.seq_lens[r], 0) + max(p.new_lens[r], 0));
+    }
+    if (tid == 0) {
+      *p.n_free_out = max(n_free - taken, 0);
+      *p.status = (taken > n_free ? BWS_KV_NO_BLOCKS : 0) | (s_over ? BWS_KV_TABLE_FULL : 0) |
+                  (total > p.n_rows ? BWS_KV_NO_ROWS : 0);
+    }
+  }
+  const int step = gridDim.x * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
+  for (long long i = first; i < taken; i += step) {
+    const int r = last_not_above(s_blk, p.R, (int)i);
+    const long long c = ((long long)max(p.seq_lens[r], 0) + p.B - 1) / p.B + (i - s_blk[r]);
+    if (c < p.max_blocks) p.table[(size_t)r * p.max_blocks + c] = i < n_free ? p.free_blocks[n_free - 1 - i] : -1;
+  }
+  for (long long t = first; t < p.n_rows; t += step) {
+    int slot = -1, pos = -1;
+    if (t < total) {
+      const int r = last_not_above(s_row, p.R, (int)t);
+      const int seq = max(p.seq_lens[r], 0);
+      const long long at = (long long)seq + (t - s_row[r]);
+      const long long c = at / p.B, have = ((long long)seq + p.B - 1) / p.B;
+      int blk = -1;
+      if (c < p.max_blocks) {
+        if (c < have) {
+          blk = p.table[(size_t)r * p.max_blocks + c];
+        } else {
+          const long long i = s_blk[r] + (c - have);
+          if (i < n_free) blk = p.free_blocks[n_free - 1 - i];
+        }
+      }
+      pos = clamp_i32(at);
+      if (blk >= 0) slot = clamp_i32((long long)blk * p.B + at % p.B);
+    }
+    p.slots[t] = slot;
+    p.positions[t] = pos;
+  }
+}
+
+// ---- norm, rotation, cache write ------------------------------------------------
+
+constexpr int kAppendThreads = 128;
+constexpr int kAppendWarps = kAppendThreads / 32;
+
+struct AppendParams {
+  bws_qkv in;
+  bws_kv_cache c;
+  uint16_t* q_out;
+  int span;          // rows whose runs one key/value CTA writes
+  int n_kv_ctas;     // spans * kv heads * 2, before the query CTAs
+  int heads_per;     // query heads a warp takes of one row
+  int stage_rows;    // rows of a run kept in shared memory between the two passes
+};
+
+BWS_DEV float bf16f(uint32_t v16) { return __uint_as_float(v16 << 16); }
+
+// A lane's E = D / 32 neighbouring values of one head.
+template <int E>
+BWS_DEV void load_head(const uint16_t* p, float (&x)[E]) {
+  uint32_t w[E / 2];
+  if constexpr (E == 2) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (E == 4) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  }
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    x[2 * i] = bf16f(w[i] & 0xFFFFu);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+template <int E>
+BWS_DEV void norm_head(float (&x)[E], const float (&w)[E], float eps) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) s = fmaf(x[i], x[i], s);
+  s = warp_sum(s);
+  const float r = rsqrtf(s * (1.0f / (32 * E)) + eps);
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] = x[i] * r * w[i];
+}
+
+// cos and sin of position * inv_freq[i] for a row's rot / 2 pairs, in turns:
+// f = inv_freq / 2 pi, and only the turn's fraction is kept. Below 2^24 the
+// position is exact in FP32 and f two FP32 parts (48 bits): the high product is
+// exact as a rounded product and its FMA remainder, so whole turns leave it
+// before the parts are added, without FP64 (which runs at about 2 a clock and
+// SM here). From 2^24 on the product is taken in FP64. Either way the fraction
+// is off by a few 2^-24.
+BWS_DEV void row_angles(int pos, const float* inv_freq, int half, float2* cs, int lane) {
+  const float fp = (float)pos;
+  const bool near = pos < (1 << 24) && pos > -(1 << 24);
+  for (int i = lane; i < half; i += 32) {
+    const double f = (double)inv_freq[i] * 0.15915494309189533577;
+    float t;
+    if (near) {
+      const float fh = (float)f, fl = (float)(f - (double)fh);
+      const float a = fh * fp, e = fmaf(fh, fp, -a);
+      t = (a - rintf(a)) + fmaf(fl, fp, e);
+      t -= rintf(t);
+    } else {
+      const double d = f * (double)pos;
+      t = (float)(d - rint(d));
+    }
+    float s, c;
+    sincospif(2.0f * t, &s, &c);
+    cs[i] = make_float2(c, s);
+  }
+}
+
+// Rotates a head held E values a lane; buf: the warp's own D floats.
+template <int E>
+BWS_DEV void rotate_head(float (&x)[E], const float2* cs, int rot, bool interleaved, float* buf, int lane) {
+  const int base = lane * E;
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      if (base + i < rot) {
+        const float2 a = cs[(base + i) >> 1];
+        const float u = x[i], v = x[i + 1];
+        x[i] = u * a.x - v * a.y;
+        x[i + 1] = v * a.x + u * a.y;
+      }
+    }
+    return;
+  }
+  __syncwarp();   // the last head's reads of buf are done
+#pragma unroll
+  for (int i = 0; i < E; ++i) buf[base + i] = x[i];
+  __syncwarp();
+  const int half = rot >> 1;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int d = base + i;
+    if (d < half) {
+      const float2 a = cs[d];
+      x[i] = x[i] * a.x - buf[d + half] * a.y;
+    } else if (d < rot) {
+      const float2 a = cs[d - half];
+      x[i] = x[i] * a.x + buf[d - half] * a.y;
+    }
+  }
+}
+
+// e of the smallest 2^e with amax <= 448 * 2^e, in [-60, 60]; 448 = 1.75 * 2^8.
+BWS_DEV int scale_exponent(float amax) {
+  if (amax == 0.0f) return -60;
+  const int x = floor_log2_abs(amax);
+  const int e = amax > ldexp_exact(1.75f, x) ? x - 7 : x - 8;
+  return min(max(e, -60), 60);
+}
+
+template <int E>
+BWS_DEV void store_codes(uint8_t* p, const float (&x)[E], float inv) {
+  uint32_t h[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) h[i] = f32x2_to_e4m3x2(x[2 * i + 1] * inv, x[2 * i] * inv);
+  if constexpr (E == 2) {
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)h[0];
+  } else if constexpr (E == 4) {
+    *reinterpret_cast<uint32_t*>(p) = h[0] | (h[1] << 16);
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  }
+}
+
+// Query CTAs: a warp takes heads_per heads of one row, whose angles it forms
+// once. Key/value CTAs: one span of rows, one kv head, one side; each run of
+// rows that starts in the span is normed and rotated by the warps, a row each,
+// its largest magnitude joined over the CTA, and written under the scale that
+// follows. Between the two passes the values wait in shared memory (the first
+// stage_rows rows; the rest, in long runs of wide heads, are formed again: the
+// rows are in L1 by then).
+// Bound: launch and three dependent loads for a decoded token, the bytes of
+// the rows for a prompt chunk.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+  constexpr int E = D / 32;
+  extern __shared__ float s_stage[];                 // [stage_rows][D]
+  __shared__ float s_buf[kAppendWarps][D];
+  __shared__ float2 s_cs[kAppendWarps][D / 2];
+  __shared__ float s_amax[kAppendWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bws_qkv& in = p.in;
+  const int half = in.rot >> 1;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if ((int)blockIdx.x >= p.n_kv_ctas) {
+    const int groups = (in.n_q_heads + p.heads_per - 1) / p.heads_per;
+    const long long unit = (long long)(blockIdx.x - p.n_kv_ctas) * kAppendWarps + warp;
+    const int row = (int)(unit / groups);
+    if (row >= in.n_rows) return;
+    const int h0 = (int)(unit % groups) * p.heads_per, h1 = min(h0 + p.heads_per, in.n_q_heads);
+    float w[E];
+    if (in.q_weight != nullptr) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) w[i] = in.q_weight[lane * E + i];
+    }
+    row_angles(in.positions[row], in.inv_freq, half, s_cs[warp], lane);
+    __syncwarp();
+    for (int h = h0; h < h1; ++h) {
+      float x[E];
+      load_head<E>(in.q + row * in.q_row_stride + h * in.q_head_stride + lane * E, x);
+      if (in.q_weight != nullptr) norm_head<E>(x, w, in.eps);
+      rotate_head<E>(x, s_cs[warp], in.rot, in.interleaved != 0, s_buf[warp], lane);
+      uint32_t o[E / 2];
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        o[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      uint16_t* dst = p.q_out + ((size_t)row * in.n_q_heads + h) * D + lane * E;
+      if constexpr (E == 2) *reinterpret_cast<uint32_t*>(dst) = o[0];
+      else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+      else *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    return;
+  }
+
+  const bws_kv_cache& c = p.c;
+  const int B = c.block_tokens, K = c.n_kv_heads;
+  const int side = blockIdx.x & 1, head = (int)(blockIdx.x >> 1) % K;
+  const int t0 = (int)((blockIdx.x >> 1) / K) * p.span, t1 = min(t0 + p.span, in.n_rows);
+  const long long n_slots = (long long)c.n_blocks * B;
+  const uint16_t* src = side ? in.v + head * in.v_head_stride : in.k + head * in.k_head_stride;
+  const long long row_stride = side ? in.v_row_stride : in.k_row_stride;
+  const bool normed = !side && in.k_weight != nullptr;
+  float w[E];
+  if (normed) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) w[i] = in.k_weight[lane * E + i];
+  }
+
+  auto form = [&](int row, float (&x)[E]) {
+    load_head<E>(src + row * row_stride + lane * E, x);
+    if (side) return;
+    if (normed) norm_head<E>(x, w, in.eps);
+    if (half > 0) {
+      __syncwarp();
+      row_angles(in.positions[row], in.inv_freq, half, s_cs[warp], lane);
+      __syncwarp();
+      rotate_head<E>(x, s_cs[warp], in.rot, in.interleaved != 0, s_buf[warp], lane);
+    }
+  };
+
+  int t = t0;
+  while (t < t1) {
+    const int slot = in.slots[t];
+    if (slot < 0 || slot >= n_slots) { ++t; continue; }
+    const int off = slot % B, room = B - off;
+    if (off != 0 && t > 0 && in.slots[t - 1] == slot - 1) { ++t; continue; }   // inside an earlier run
+    int m = 1;   // the run's rows: slots go on by one, inside the block
+    while (m < room) {
+      const int i = m + lane;
+      const bool on = i < room && t + i < in.n_rows && in.slots[t + i] == slot + i;
+      const unsigned b = __ballot_sync(0xffffffffu, on);
+      const int n = b == 0xffffffffu ? 32 : __ffs(~b) - 1;
+      m += n;
+      if (n < 32) break;
+    }
+    float amax = 0.0f;
+    for (int i = warp; i < m; i += kAppendWarps) {
+      float x[E];
+      form(t + i, x);
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const float a = fabsf(x[k]);
+        if (a < INFINITY) amax = fmaxf(amax, a);   // NaN and infinity set no scale
+      }
+      if (i < p.stage_rows) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) s_stage[i * D + lane * E + k] = x[k];
+      }
+    }
+    amax = warp_max(amax);
+    if (lane == 0) s_amax[warp] = amax;
+    const int block = slot / B;
+    float* scale_at = (side ? c.v_scale : c.k_scale) + (size_t)block * K + head;
+    const float old = *scale_at;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAppendWarps; ++i) amax = fmaxf(amax, s_amax[i]);
+    const float need = exp2i(scale_exponent(amax));
+    const float scale = off == 0 ? need : fmaxf(old, need);
+    const float inv = 1.0f / scale;
+    uint8_t* codes = (side ? c.v : c.k) + (size_t)block * c.block_stride + (size_t)head * c.head_stride;
+    if (off != 0 && scale != old) {   // the scale grew: the block's earlier codes again, under it
+      const float f = old / scale;
+      uint32_t* w32 = reinterpret_cast<uint32_t*>(codes);
+      for (int i = threadIdx.x; i < off * (D / 4); i += kAppendThreads) {
+        uint32_t lo, hi;
+        e4m3x4_to_f16x2x2(w32[i], lo, hi);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+        w32[i] = f32x2_to_e4m3x2(a.y * f, a.x * f) | (f32x2_to_e4m3x2(b.y * f, b.x * f) << 16);
+      }
+    }
+    for (int i = warp; i < m; i += kAppendWarps) {
+      float x[E];
+      if (i < p.stage_rows) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) x[k] = s_stage[i * D + lane * E + k];
+      } else {
+        form(t + i, x);
+      }
+      store_codes<E>(codes + (size_t)(off + i) * D + lane * E, x, inv);
+    }
+    __syncthreads();   // every thread has read the old scale and s_amax
+    if (threadIdx.x == 0) *scale_at = scale;
+    t += m;
+  }
+}
+
+template <typename K, typename P>
+cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t st, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+int check_kv_cache(const bws_kv_cache* c, const char* name) {
+  if (c == nullptr) return fail(BWS_ERR_INVALID_ARG, "%s: null cache", name);
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: head_dim = %d must be 64, 128 or 256", name, c->head_dim);
+  if (c->block_tokens < 16 || c->block_tokens > 256 || c->block_tokens % 16 != 0)
+    return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: block_tokens = %d must be a multiple of 16 in [16, 256]", name,
+                c->block_tokens);
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 128)
+    return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: n_kv_heads = %d must be in [1, 128]", name, c->n_kv_heads);
+  if (c->n_blocks < 1 || (long long)c->n_blocks * c->block_tokens >= (1LL << 31))
+    return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: n_blocks = %d (1 or more, below 2^31 tokens)", name, c->n_blocks);
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return fail(BWS_ERR_INVALID_ARG, "%s: null cache pointer", name);
+  const size_t rows = (size_t)c->block_tokens * c->head_dim;
+  if (c->block_stride % 16 || c->head_stride % 16 || !aligned(c->k, 16) || !aligned(c->v, 16) ||
+      !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+    return fail(BWS_ERR_MISALIGNED, "%s: cache codes and strides 16-byte, scales 4-byte alignment needed", name);
+  // blocks and heads must not overlap: [blocks][heads] or [heads][blocks] order
+  const bool by_block = c->head_stride >= rows && c->block_stride >= c->head_stride * (c->n_kv_heads - 1) + rows;
+  const bool by_head = c->block_stride >= rows && c->head_stride >= c->block_stride * ((size_t)c->n_blocks - 1) + rows;
+  if (!(by_block || by_head) || c->block_stride >= (1ull << 40) || c->head_stride >= (1ull << 40))
+    return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: cache strides (%zu, %zu) overlap or are out of range", name,
+                c->block_stride, c->head_stride);
+  return BWS_OK;
+}
+
+}  // namespace bws
+
+extern "C" {
+
+int bws_kv_plan(const int32_t* seq_lens, const int32_t* new_lens, int n_requests, int block_tokens,
+                int32_t* block_table, int max_blocks, const int32_t* free_blocks, const int32_t* n_free, int n_rows,
+                int32_t* slots, int32_t* positions, int32_t* row_start, int32_t* kv_lens, int32_t* n_free_out,
+                int32_t* status, void* stream) {
+  using namespace bws;
+  const char* name = "bws_kv_plan";
+  if (n_requests < 0 || n_requests > kPlanMaxRequests)
+    return fail(BWS_ERR_INVALID_ARG, "%s: n_requests = %d must be in [0, %d]", name, n_requests, kPlanMaxRequests);
+  if (n_rows < 0 || max_blocks < 0)
+    return fail(BWS_ERR_INVALID_ARG, "%s: n_rows = %d, max_blocks = %d", name, n_rows, max_blocks);
+  if (block_tokens < 16 || block_tokens > 256 || block_tokens % 16 != 0)
+    return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: block_tokens = %d must be a multiple of 16 in [16, 256]", name,
+                block_tokens);
+  if (!n_free || !row_start || !n_free_out || !status || (n_requests > 0 && (!seq_lens || !new_lens || !kv_lens)) ||
+      (n_requests > 0 && max_blocks > 0 && (!block_table || !free_blocks)) || (n_rows > 0 && (!slots || !positions)))
+    return fail(BWS_ERR_INVALID_ARG, "%s: null pointer", name);
+  if (n_free == n_free_out) return fail(BWS_ERR_INVALID_ARG, "%s: n_free_out must not be n_free", name);
+  const void* ptrs[] = {seq_lens, new_lens, block_table, free_blocks, n_free, slots, positions, row_start, kv_lens,
+                        n_free_out, status};
+  for (const void* q : ptrs)
+    if (!aligned(q, 4)) return fail(BWS_ERR_MISALIGNED, "%s: 4-byte alignment needed", name);
+  PlanParams p = {seq_lens, new_lens, n_requests, block_tokens, block_table, max_blocks, free_blocks, n_free, n_rows,
+                  slots, positions, row_start, kv_lens, n_free_out, status};
+  // four rows a thread, up to two CTAs an SM
+  const long long want = ((long long)n_rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  const long long most = 2LL * num_sms();
+  const unsigned grid = (unsigned)(want < 1 ? 1 : want > most ? most : want);
+  return cuda_status(launch_pdl(plan_kernel, grid, kPlanThreads, 2 * sizeof(int) * ((size_t)n_requests + 1),
+                                as_stream(stream), p), name);
+}
+
+int bws_qk_norm_rope_append(const bws_qkv* in, const bws_kv_cache* cache, uint16_t* q_out, void* stream) {
+  using namespace bws;
+  const char* name = "bws_qk_norm_rope_append";
+  if (in == nullptr) return fail(BWS_ERR_INVALID_ARG, "%s: null input", name);
+  const int rc = check_kv_cache(cache, name);
+  if (rc) return rc;
+  const int D = cache->head_dim, K = cache->n_kv_heads, H = in->n_q_heads;
+  if (in->n_rows < 0 || H < 1 || H > 1024)
+    return fail(BWS_ERR_INVALID_ARG, "%s: n_rows = %d, n_q_heads = %d (1..1024)", name, in->n_rows, H);
+  if (in->rot < 0 || in->rot > D || in->rot % 2)
+    return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: rot = %d must be even and at most head_dim", name, in->rot);
+  if (in->n_rows == 0) {
+    clear_error();
+    return BWS_OK;
+  }
+  if (!in->q || !in->k || !in->v || !in->positions || !in->slots || !q_out || (in->rot > 0 && !in->inv_freq))
+    return fail(BWS_ERR_INVALID_ARG, "%s: null pointer", name);
+  if (!(in->eps >= 0.0f)) return fail(BWS_ERR_INVALID_ARG, "%s: eps must not be negative", name);
+  if (!aligned(in->q, 16) || !aligned(in->k, 16) || !aligned(in->v, 16) || !aligned(q_out, 16) ||
+      !aligned(in->positions, 4) || !aligned(in->slots, 4) || !aligned(in->inv_freq, 4) ||
+      !aligned(in->q_weight, 4) || !aligned(in->k_weight, 4))
+    return fail(BWS_ERR_MISALIGNED, "%s: rows 16-byte, other pointers 4-byte alignment needed", name);
+  const int64_t strides[] = {in->q_row_stride, in->q_head_stride, in->k_row_stride,
+                             in->k_head_stride, in->v_row_stride, in->v_head_stride};
+  for (int64_t s : strides)
+    if (s % 8 != 0) return fail(BWS_ERR_MISALIGNED, "%s: strides must be multiples of 8 elements", name);
+  AppendParams p;
+  p.in = *in;
+  p.c = *cache;
+  p.q_out = q_out;
+  const long long sms = num_sms();
+  // A span of one row gives every row of a decode batch its own CTA; longer
+  // calls take whole blocks, so that no CTA is launched only to find that its
+  // rows belong to an earlier run.
+  const long long rows = in->n_rows;
+  long long span = rows * K * 2 / (sms * 16);
+  span = span < 1 ? 1 : span > cache->block_tokens ? cache->block_tokens : span;
+  p.span = (int)span;
+  const long long spans = (rows + span - 1) / span;
+  const long long kv_ctas = spans * K * 2;
+  // heads of a row that share a warp's angles, as long as every SM keeps 16 warps
+  long long per = rows * H / (sms * 16);
+  per = per < 1 ? 1 : per > 8 ? 8 : per;
+  p.heads_per = (int)per;
+  const long long groups = (H + per - 1) / per;
+  const long long q_ctas = (rows * groups + kAppendWarps - 1) / kAppendWarps;
+  if (kv_ctas + q_ctas >= (1LL << 31)) return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: too many rows", name);
+  p.n_kv_ctas = (int)kv_ctas;
+  long long stage = 32 * 1024 / (4 * D);
+  if (stage > cache->block_tokens) stage = cache->block_tokens;
+  if (stage > rows) stage = rows;
+  p.stage_rows = (int)stage;
+  const size_t smem = (size_t)stage * D * 4;
+  const unsigned grid = (unsigned)(kv_ctas + q_ctas);
+  cudaStream_t st = as_stream(stream);
+  cudaError_t e;
+  if (D == 64) e = launch_pdl(append_kernel<64>, grid, kAppendThreads, smem, st, p);
+  else if (D == 128) e = launch_pdl(append_kernel<128>, grid, kAppendThreads, smem, st, p);
+  else e = launch_pdl(append_kernel<256>, grid, kAppendThreads, smem, st, p);
+  return cuda_status(e, name);
+}
+
+}  // extern "C"

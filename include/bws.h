@@ -438,6 +438,142 @@ int bws_decode_step_tap(bws_stack_plan* plan, const uint16_t* x0, float* logits,
                         size_t tap_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* The step's attention state: an 8-bit key/value cache, and drafted tokens  */
+/* ------------------------------------------------------------------------ */
+
+/* A key/value cache in blocks of tokens, held as E4M3 codes with one FP32
+ * scale per (block, kv head) and side: key = k_scale * dec(code). The pages
+ * name the cache's bytes ([LingMoE] section 13) but no format; this one keeps
+ * a power of two as the scale, so that a scale that grows moves the codes
+ * already written by an exact shift (but for the smallest, which round).
+ * Token t of a request lives in slot table[t / block_tokens] * block_tokens +
+ * t % block_tokens. Codes of one (block, head) are block_tokens contiguous
+ * rows of head_dim bytes; blocks and heads may lie at any stride. */
+typedef struct bws_kv_cache {
+  int n_blocks;            /* n_blocks * block_tokens < 2^31                   */
+  int n_kv_heads;          /* 1..128                                           */
+  int block_tokens;        /* 16..256, % 16 == 0                               */
+  int head_dim;            /* 64, 128 or 256                                   */
+  uint8_t* k;              /* codes, 16-byte aligned                           */
+  uint8_t* v;              /* same strides as k                                */
+  float* k_scale;          /* [n_blocks][n_kv_heads], in [2^-60, 2^60]         */
+  float* v_scale;
+  size_t block_stride;     /* bytes from block to block, % 16 == 0             */
+  size_t head_stride;      /* bytes from head to head, % 16 == 0               */
+} bws_kv_cache;
+
+enum bws_kv_plan_status {  /* bits of bws_kv_plan's status                     */
+  BWS_KV_NO_BLOCKS = 1,    /* the free list ran out: entries and slots are -1  */
+  BWS_KV_TABLE_FULL = 2,   /* a request is longer than its table row           */
+  BWS_KV_NO_ROWS = 4       /* more new tokens than n_rows                      */
+};
+
+/* Block tables and slot maps from request lengths, on the device. Request r
+ * holds seq_lens[r] tokens and gets new_lens[r] more (negative counts as 0).
+ * Its table row gains the entries [ceil(seq/B), ceil((seq+new)/B)), taken from
+ * the end of free_blocks[0, n_free) in request order; entries below are read,
+ * entries above are left. Row row_start[r] + j (j < new_lens[r]) gets position
+ * seq_lens[r] + j and that token's slot; rows past the last, and tokens
+ * without a block, get slot -1 (position -1 past the last row), which
+ * bws_qk_norm_rope_append skips.
+ *   seq_lens, new_lens int32 [n_requests]; block_table int32
+ *   [n_requests][max_blocks] in/out; free_blocks int32 (n_free entries);
+ *   n_free int32 [1]; slots, positions int32 [n_rows] out; row_start int32
+ *   [n_requests + 1] out; kv_lens int32 [n_requests] out (seq + new);
+ *   n_free_out int32 [1] out (not n_free itself); status int32 [1] out
+ *   (bws_kv_plan_status bits). All device pointers.
+ * 0 <= n_requests <= 4096, n_rows >= 0, block_tokens as bws_kv_cache. The call
+ * changes only its outputs and the table, so it can run again. One kernel. */
+int bws_kv_plan(const int32_t* seq_lens, const int32_t* new_lens, int n_requests,
+                int block_tokens, int32_t* block_table, int max_blocks,
+                const int32_t* free_blocks, const int32_t* n_free, int n_rows,
+                int32_t* slots, int32_t* positions, int32_t* row_start,
+                int32_t* kv_lens, int32_t* n_free_out, int32_t* status,
+                void* stream);
+
+/* Per-head RMS norm of queries and keys, their rotation by position, and the
+ * write of keys and values into the cache, in one pass. Per head, in FP32:
+ *   y = x / sqrt(mean(x^2) + eps) * weight    (weight NULL: y = x, no norm)
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin) for rot/2 pairs,
+ *   angle = positions[row] * inv_freq[pair], pair i = (i, i + rot/2), or
+ *   (2i, 2i + 1) if interleaved; dimensions >= rot pass.
+ * The angle's turn is reduced without loss at far positions. Queries are
+ * rounded to BF16; keys and values (not normed, not rotated) to E4M3 under
+ * their block's scale. Rows that fill one block must follow each other (slots
+ * s, s + 1, ...), as bws_kv_plan makes them; such a run sets, per kv head,
+ *   need  = 2^e, the smallest that holds the run's largest finite magnitude
+ *           (<= 448 * 2^e), e in [-60, 60]
+ *   scale = need if the run starts the block, else max(scale, need),
+ * and rounds the block's earlier codes again where the scale grew. Values past
+ * the scale's reach saturate at 448; NaN stays NaN. Rows with a slot < 0 or
+ * past the cache give a query row but write nothing.
+ *   q bf16 [n_rows][n_q_heads][head_dim], k, v bf16 [n_rows][n_kv_heads]
+ *   [head_dim]: innermost contiguous, row and head strides in elements,
+ *   multiples of 8, pointers 16-byte aligned; positions, slots int32 [n_rows];
+ *   q_weight, k_weight fp32 [head_dim] or NULL; inv_freq fp32 [rot/2] (rot
+ *   even, 0..head_dim); q_out bf16 [n_rows][n_q_heads][head_dim].
+ * n_rows == 0 is a no-op. One kernel, no workspace. */
+typedef struct bws_qkv {
+  const uint16_t* q; int64_t q_row_stride, q_head_stride;
+  const uint16_t* k; int64_t k_row_stride, k_head_stride;
+  const uint16_t* v; int64_t v_row_stride, v_head_stride;
+  int n_rows, n_q_heads;
+  const int32_t* positions; const int32_t* slots;
+  const float* q_weight; const float* k_weight;
+  const float* inv_freq; int rot; int interleaved; float eps;
+} bws_qkv;
+int bws_qk_norm_rope_append(const bws_qkv* in, const bws_kv_cache* cache,
+                            uint16_t* q_out, void* stream);
+
+/* Attention of each request's last 1..8 tokens over the cache:
+ *   out[row] = sum_t softmax_t(scale * q . key_t) value_t
+ * over tokens t <= kv_lens[r] - n_r + j for row j of request r's n_r =
+ * row_start[r+1] - row_start[r] rows (so the rows are the request's last
+ * tokens, already in the cache). Query head h reads kv head h / (n_q_heads /
+ * n_kv_heads). A row that sees no token gives 0 (lse -inf). Codes are exact in
+ * the products; sums and softmax statistics are FP32. Table entries outside
+ * the cache count as tokens that are not there.
+ *   q bf16 [n_rows][n_q_heads][head_dim], innermost contiguous, strides in
+ *   elements (multiples of 8), 16-byte aligned; block_table int32 [n_requests]
+ *   [max_blocks]; row_start int32 [n_requests + 1]; kv_lens int32
+ *   [n_requests]; out bf16 [n_rows][n_q_heads][head_dim]; lse fp32 [n_rows]
+ *   [n_q_heads] (log of the sum of exponentials) or NULL. Device pointers; the
+ *   lengths are read on the device, so a captured call follows them.
+ * 1 <= max_rows <= 8 bounds the rows of a request, n_q_heads / n_kv_heads in
+ * 1..16. Workspace: bws_kv_attention_workspace_size() bytes, 256-byte aligned;
+ * bws_status_word reports a bounded wait that ran out. Two kernels. */
+size_t bws_kv_attention_workspace_size(int n_q_heads, int n_kv_heads, int head_dim, int max_rows);
+int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride,
+                     int n_rows, int n_q_heads, const bws_kv_cache* cache,
+                     const int32_t* block_table, int max_blocks, int n_requests,
+                     const int32_t* row_start, const int32_t* kv_lens, int max_rows,
+                     float scale, uint16_t* out, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Verification of drafted tokens against the target's probabilities
+ * ([Spark27B] "More tokens per weight read": the drafts that agree with the
+ * target stand, and one more token is drawn). Request r's rows are row_start[r]
+ * .. row_start[r+1] - 1: the last has no draft, row i before it drafted
+ * tokens[i]. In row order, draft x stands while accept_u[i] * q_i(x) < p_i(x);
+ * at the first that does not, and after the last, one token is drawn from
+ *   w = max(p - q, 0) in FP32 (p where that is 0 everywhere), or p
+ * as the first v with w[0] + .. + w[v] > sample_u[r] * sum(w). Sums carry 48
+ * bits or more. Weights that are negative or NaN count as 0.
+ *   target fp32 [n_rows][vocab], draft fp32 [n_rows][vocab] or NULL (each draft
+ *   was certain: q is 1 at the token), rows at target_stride / draft_stride
+ *   elements; tokens int32, accept_u fp32 [n_rows]; sample_u fp32 [n_requests]
+ *   (uniform numbers in [0, 1)); out int32 [n_requests][max_rows]: the drafts
+ *   that stand, the drawn token, then -1; n_out int32 [n_requests] (0 for a
+ *   request without rows). A token outside the vocabulary does not stand; a
+ *   row without a positive weight draws -1.
+ * 1 <= max_rows <= 32 bounds the rows of a request. One kernel. */
+int bws_draft_verify(const float* target, int64_t target_stride, const float* draft,
+                     int64_t draft_stride, const int32_t* tokens, int n_rows, int vocab,
+                     const int32_t* row_start, int n_requests, const float* accept_u,
+                     const float* sample_u, int max_rows, int32_t* out, int32_t* n_out,
+                     void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Status and measurement                                                    */
 /* ------------------------------------------------------------------------ */
 
