@@ -5,9 +5,9 @@
 // product of two FP32 numbers is exact in FP64, so the test has no rounding);
 // the number that stand picks the row to draw from, whose w = max(p - q, 0) the
 // cluster sums once: every warp owns a contiguous range of the vocabulary and
-// keeps its sum. CTA 0 collects the warps' sums over distributed shared memory,
-// finds the range in which the running sum passes u * total, and reads only
-// that range again (a few hundred words, now in L2) to find the token.
+// sends its sum to every CTA over distributed shared memory. CTA 0 finds the
+// range in which the running sum passes u * total and reads only that one again
+// (now in L2), first by sixteenths, a warp each, then word by word.
 // A lane adds FP32 numbers in two words (the rounded sum and what the rounding
 // left), which carries 48 bits: on this GPU FP64 adds run at a small fraction
 // of the FP32 rate and would set the time (1.3 FP64 adds per 4-byte word
@@ -132,13 +132,56 @@ BWS_DEV double warp_scan(double x, int lane) {
   return x;
 }
 
+BWS_DEV double sum_of(const VerifyParams& p, const Row& row, int a, int b, int lane) {
+  if (p.vec)
+    return row.q != nullptr ? range_sum<true, true>(row, a, b, lane) : range_sum<true, false>(row, a, b, lane);
+  return row.q != nullptr ? range_sum<false, true>(row, a, b, lane) : range_sum<false, false>(row, a, b, lane);
+}
+
+// One warp: the first of n (a multiple of 16, at most 256) ranges whose running
+// sum passes target(total); else, where rounding leaves none, the last that has
+// any weight; -1 if no range has. *before: the sum of the ranges ahead of it.
+template <class F>
+BWS_DEV int pick_range(const double* sums, int n, F target, double* before, int lane) {
+  constexpr int kMost = kVerifyMaxCluster * kVerifyWarps / 32;
+  const int each = (n + 31) / 32;
+  double x[kMost], mine = 0.0;   // a lane's ranges, in order
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int k = lane * each + i;
+    x[i] = i < each && k < n ? sums[k] : 0.0;
+    mine += x[i];
+  }
+  const double upto = warp_scan(mine, lane);
+  const double t = target(__shfl_sync(0xffffffffu, upto, 31));
+  double run = upto - mine, found_at = 0.0, last_at = 0.0;
+  int found = -1, last = -1;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    if (x[i] > 0.0) {
+      last = lane * each + i;
+      last_at = run;
+      if (found < 0 && run + x[i] > t) {
+        found = last;
+        found_at = run;
+      }
+    }
+    run += x[i];
+  }
+  const unsigned fb = __ballot_sync(0xffffffffu, found >= 0), lb = __ballot_sync(0xffffffffu, last >= 0);
+  const int from = fb != 0u ? __ffs(fb) - 1 : lb != 0u ? 31 - __clz(lb) : 0;
+  *before = __shfl_sync(0xffffffffu, fb != 0u ? found_at : last_at, from);
+  return __shfl_sync(0xffffffffu, fb != 0u ? found : last, from);
+}
+
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p) {
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ double s_sum[kVerifyWarps];
+  __shared__ double s_sum[kVerifyMaxCluster * kVerifyWarps], s_part[kVerifyWarps];
   __shared__ int s_stand;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int r = (int)blockIdx.x / n_cta;
+  cluster.barrier_arrive();   // every CTA has started before any writes to another
   pdl_launch_dependents();
   pdl_wait();
   const int start = min(max(p.row_start[r], 0), p.n_rows);
@@ -148,6 +191,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
       for (int i = threadIdx.x; i < p.max_rows; i += kVerifyThreads) p.out[(size_t)r * p.max_rows + i] = -1;
       if (threadIdx.x == 0) p.n_out[r] = 0;
     }
+    cluster.barrier_wait();
     return;
   }
   int token = -1;   // lane i of warp 0: draft i
@@ -179,74 +223,52 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
   const int quads = (p.vocab + 3) / 4, per = (quads + n_warps - 1) / n_warps;
   const int w = rank * kVerifyWarps + warp;
   auto range_begin = [&](int i) { return (int)min((long long)i * per * 4, (long long)p.vocab); };
-  double total = 0.0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    const int a = range_begin(w), b = range_begin(w + 1);
-    double s;
-    if (p.vec) s = row.q != nullptr ? range_sum<true, true>(row, a, b, lane) : range_sum<true, false>(row, a, b, lane);
-    else s = row.q != nullptr ? range_sum<false, true>(row, a, b, lane) : range_sum<false, false>(row, a, b, lane);
-    if (lane == 0) s_sum[warp] = s;
+    const double s = sum_of(p, row, range_begin(w), range_begin(w + 1), lane);
+    if (pass == 0) cluster.barrier_wait();
+    // every CTA gets every warp's sum: none reads another's memory afterwards
+    if (lane < n_cta) cluster.map_shared_rank(s_sum, lane)[w] = s;
     cluster.sync();
     if (row.q == nullptr && row.certain < 0) break;
-    // Is anything left of the target? Every CTA asks, so that all go on alike.
-    double any = 0.0;
-    for (int i = lane; i < n_warps; i += 32)
-      any = fmax(any, cluster.map_shared_rank(s_sum, i / kVerifyWarps)[i % kVerifyWarps]);
-    if (__any_sync(0xffffffffu, any > 0.0)) break;
+    bool any = false;   // is anything left of the target?
+    for (int i = lane; i < n_warps; i += 32) any |= s_sum[i] > 0.0;
+    if (__any_sync(0xffffffffu, any)) break;
     row.q = nullptr;
     row.certain = -1;
     cluster.sync();   // every read of the sums, before they are formed again
   }
-  if (rank == 0 && warp == 0) {
-    // a lane holds the sums of n_cta * kVerifyWarps / 32 ranges in order
-    const int each = (n_warps + 31) / 32;
-    double mine = 0.0;
-    for (int i = 0; i < each; ++i) {
-      const int k = lane * each + i;
-      if (k < n_warps) mine += cluster.map_shared_rank(s_sum, k / kVerifyWarps)[k % kVerifyWarps];
-    }
-    const double upto = warp_scan(mine, lane);
-    total = __shfl_sync(0xffffffffu, upto, 31);
-    const double t = (double)p.sample_u[r] * total;
-    // the first range whose running sum passes t; else the last that has any
-    double run = upto - mine, before = 0.0, last_before = 0.0;
-    int found = -1, last = -1;
-    for (int i = 0; i < each; ++i) {
-      const int k = lane * each + i;
-      const double s = k < n_warps ? cluster.map_shared_rank(s_sum, k / kVerifyWarps)[k % kVerifyWarps] : 0.0;
-      if (s > 0.0) {
-        last = k;
-        last_before = run;
-        if (found < 0 && run + s > t) { found = k; before = run; }
-      }
-      run += s;
-    }
-    const unsigned fb = __ballot_sync(0xffffffffu, found >= 0), lb = __ballot_sync(0xffffffffu, last >= 0);
-    int k = -1;
-    if (fb != 0u) {
-      const int src = __ffs(fb) - 1;
-      k = __shfl_sync(0xffffffffu, found, src);
-      before = __shfl_sync(0xffffffffu, before, src);
-    } else if (lb != 0u) {
-      const int src = 31 - __clz(lb);
-      k = __shfl_sync(0xffffffffu, last, src);
-      before = __shfl_sync(0xffffffffu, last_before, src);
-    }
-    int drawn = -1;
-    if (k >= 0) {
-      const int a = range_begin(k), b = range_begin(k + 1);
-      double base = before;
+  if (rank != 0) return;
+
+  // ---- CTA 0: the range in which the running sum passes u * total ...
+  double before, t;
+  int k = pick_range(s_sum, n_warps, [&](double total) { return t = (double)p.sample_u[r] * total; }, &before, lane);
+  int drawn = -1;
+  if (k >= 0) {   // the same in every warp
+    // ... its sixteenths, a warp each, and the one in which it passes
+    const int a = range_begin(k), b = range_begin(k + 1);
+    const int part = ((b - a + 4 * kVerifyWarps - 1) / (4 * kVerifyWarps)) * 4;
+    const int a1 = min(a + warp * part, b), b1 = min(a1 + part, b);
+    const double s = sum_of(p, row, a1, b1, lane);
+    if (lane == 0) s_part[warp] = s;
+    __syncthreads();
+    if (warp != 0) return;
+    double before1;
+    const int k1 = pick_range(s_part, kVerifyWarps, [&](double) { return t - before; }, &before1, lane);
+    // ... and the word
+    if (k1 >= 0) {
+      const int a2 = min(a + k1 * part, b), b2 = min(a2 + part, b);
+      double base = before1;
+      const double left = t - before;
       int fallback = -1;
-      for (int v0 = a; v0 < b && drawn < 0; v0 += 128) {
+      for (int v0 = a2; v0 < b2 && drawn < 0; v0 += 128) {
         const int v = v0 + lane * 4;
         float x[4];
         double own = 0.0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = v + i < b ? weight_at(row, v + i) : 0.0f;
-          own += x[i];
-        }
+        for (int i = 0; i < 4; ++i) x[i] = v + i < b2 ? weight_at(row, v + i) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) own += x[i];
         const double scan = warp_scan(own, lane);
         double at = base + (scan - own);
         int mine_v = -1, mine_last = -1;
@@ -255,7 +277,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
           at += x[i];
           if (x[i] > 0.0f) {
             mine_last = v + i;
-            if (mine_v < 0 && at > t) mine_v = v + i;
+            if (mine_v < 0 && at > left) mine_v = v + i;
           }
         }
         const unsigned hit = __ballot_sync(0xffffffffu, mine_v >= 0), any = __ballot_sync(0xffffffffu, mine_last >= 0);
@@ -265,15 +287,16 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
       }
       if (drawn < 0) drawn = fallback;
     }
-    if (lane < p.max_rows) {
-      int32_t v = -1;
-      if (lane < stand) v = token;
-      else if (lane == stand) v = drawn;
-      p.out[(size_t)r * p.max_rows + lane] = v;
-    }
-    if (lane == 0) p.n_out[r] = stand + 1;
+  } else if (warp != 0) {
+    return;
   }
-  cluster.sync();   // no CTA leaves while its sums may be read
+  if (lane < p.max_rows) {
+    int32_t v = -1;
+    if (lane < stand) v = token;
+    else if (lane == stand) v = drawn;
+    p.out[(size_t)r * p.max_rows + lane] = v;
+  }
+  if (lane == 0) p.n_out[r] = stand + 1;
 }
 
 }  // namespace

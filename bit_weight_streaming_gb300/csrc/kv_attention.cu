@@ -68,6 +68,7 @@ struct AttnParams {
   uint32_t* failed;   // [CTAs]
   uint32_t* hdr;
   int n_ctas, least;  // CTAs; smallest share in units
+  int lead;           // what a segment costs beside its units, in units
 };
 
 // ---- the line of units -----------------------------------------------------------
@@ -87,23 +88,33 @@ BWS_DEV Request request_of(const AttnParams& p, int r, int group_rows) {
   return q;
 }
 
-BWS_DEV long long units_of(const AttnParams& p, const Request& q) { return (long long)p.K * q.groups * q.units; }
+BWS_DEV long long length_of(const AttnParams& p, const Request& q) {
+  return (long long)p.K * q.groups * (p.lead + q.units);
+}
+
+// One CTA's part of a segment: units [first, last).
+struct Segment {
+  Request rq;
+  int r, head, row0, first, last;
+  bool whole;      // the CTA has every unit
+  bool starts;     // the CTA has the first unit
+};
 
 struct Line {
   long long total, share;
-  int r;            // request that holds the asked unit
-  long long base;   // its first unit
+  int r;            // request that holds the asked position
+  long long base;   // its first position
 };
 
-// The whole CTA: total units, share, and the request of unit pick(share)
-// (clamped to the line).
+// The whole CTA: the line's length, the share, and the request at position
+// pick(share), if the line has it.
 template <class Pick>
 BWS_DEV Line find_on_line(const AttnParams& p, int group_rows, Pick pick, long long* s_warp, long long* s_found) {
   const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.R + n - 1) / n;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += units_of(p, request_of(p, r, group_rows));
+  for (int r = r0; r < r1; ++r) mine += length_of(p, request_of(p, r, group_rows));
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -126,7 +137,7 @@ BWS_DEV Line find_on_line(const AttnParams& p, int group_rows, Pick pick, long l
     long long b = before;
     int r = r0;
     for (; r < r1 - 1; ++r) {
-      const long long k = units_of(p, request_of(p, r, group_rows));
+      const long long k = length_of(p, request_of(p, r, group_rows));
       if (u < b + k) break;
       b += k;
     }
@@ -178,14 +189,18 @@ struct Shape {
   static constexpr int kPanels = D / kRowBytes;               // panels of 16 tokens x kRowBytes
   static constexpr int kSide = kUnit * D;                     // bytes of a unit's keys, or values
   static constexpr int kStage = 2 * kSide;
-  // A ring at least as deep as a warp's O in FP32 (the segment's end reuses
-  // it), three stages or 12 KB at the least: two CTAs an SM then keep 96 KB or
-  // more in flight, well above the 36 KB that HBM's latency asks of an SM.
-  static constexpr int kStages = NT > 3 ? (D == 64 && NT < 6 ? 6 : NT) : (D == 64 ? 6 : 3);
-  static constexpr int kRing = kStages * kStage;
   static constexpr int kRows = 8 * NT;
+  static constexpr int kJoin = kRows * D * 4;                 // a warp's O in FP32, for the segment's end
+  // Up to NT * D = 256 the warps' O has memory of its own, so that the next
+  // segment's copies run during the join; wider ones use the drained ring.
+  static constexpr bool kOverlap = NT * D <= 256;
+  static constexpr int kCtas = NT * D <= 128 ? 2 : 1;         // CTAs an SM, by registers
+  static constexpr int kStages = !kOverlap ? NT + (D == 256) : ((kCtas == 2 ? 96 : 192) * 1024 / kAttnWarps - kJoin) / kStage;
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kWarpBytes = kRing + (kOverlap ? kJoin : 0);
   static constexpr bool kQInRegs = NT * D <= 256;
   static constexpr int kQStride = 2 * D + 16;                 // bytes of a query row, off the banks' period
+  static_assert(kStages >= 2 && (kOverlap || kRing >= kJoin), "ring");
 };
 
 template <int D, int NT>
@@ -194,8 +209,7 @@ struct __align__(16) Tail {
   float q_scale[8 * NT];
   float m[kAttnWarps][8 * NT];
   float l[kAttnWarps][8 * NT];
-  uint32_t nan_mask[D];                                       // bit j: token j of the rows' own has a NaN there
-  float2 scales[kAttnWarps][Shape<D, NT>::kStages];           // ks, vs; ks = -1: the block is not there
+  uint32_t nan_mask[2][D];                                    // bit j: token j of the rows' own has a NaN there
   unsigned long long full[kAttnWarps][Shape<D, NT>::kStages];
   long long line_warp[kAttnWarps];
   long long line_found[2];
@@ -210,16 +224,18 @@ BWS_DEV uint32_t chunk_at(int row, int c) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kRing * kAttnWarps <= 100 * 1024 ? 2 : 1)
-attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel(const __grid_constant__ AttnParams p) {
   using S = Shape<D, NT>;
   constexpr int kMT = D / 16;   // m tiles of O^T
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  Tail<D, NT>& T = *reinterpret_cast<Tail<D, NT>*>(smem_raw + (base - smem_u32(smem_raw)) + S::kRing * kAttnWarps);
+  unsigned char* const smem = smem_raw + (base - smem_u32(smem_raw));   // rings, then the warps' O, then the tail
+  Tail<D, NT>& T = *reinterpret_cast<Tail<D, NT>*>(smem + S::kWarpBytes * kAttnWarps);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const uint32_t ring = base + warp * S::kRing;
+  float* const join = reinterpret_cast<float*>(smem + (S::kOverlap ? S::kRing * kAttnWarps : 0));
+  constexpr int kJoinStep = (S::kOverlap ? S::kJoin : S::kRing) / 4;    // floats from warp to warp
   const uint32_t bar0 = smem_u32(&T.full[warp][0]);
   if (lane == 0) {
     for (int s = 0; s < S::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
@@ -237,96 +253,135 @@ attn_kernel(const __grid_constant__ AttnParams p) {
   // this lane's ldmatrix row: tokens 0-7 and 8-15 of one chunk, then of the next
   const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lchunk = lane >> 4;
 
-  int r = line.r;
-  long long rbase = line.base;
-  long long u = u0;
-  while (u < u1) {
-    const Request rq = request_of(p, r, S::kRows);
-    const long long rn = units_of(p, rq);
-    if (u >= rbase + rn) {   // on to the next request
-      rbase += rn;
-      ++r;
-      continue;
+  // ---- the CTA's segments, one after the other
+  long long u = u0, rbase = line.base;
+  int at_r = line.r;
+  Segment sg;
+  auto next_segment = [&]() {   // false: the share is done
+    while (u < u1) {
+      const Request rq = request_of(p, at_r, S::kRows);
+      const long long rn = length_of(p, rq);
+      if (u >= rbase + rn) {
+        rbase += rn;
+        ++at_r;
+        continue;
+      }
+      const int len = p.lead + rq.units, seg = (int)((u - rbase) / len);
+      const long long a = rbase + (long long)seg * len, b = a + len, first_unit = a + p.lead;
+      const long long from = max(u, first_unit), to = min(u1, b);
+      u = to;
+      if (from >= to) continue;   // the share ends before the first unit
+      sg.rq = rq;
+      sg.r = at_r;
+      sg.head = seg / rq.groups;
+      sg.row0 = (seg % rq.groups) * S::kRows;
+      sg.first = (int)(from - first_unit);
+      sg.last = (int)(to - first_unit);
+      sg.starts = first_unit >= u0;
+      sg.whole = sg.starts && to == b;
+      return true;
     }
-    const int seg = (int)((u - rbase) / rq.units);
-    const long long seg_a = rbase + (long long)seg * rq.units, seg_b = seg_a + rq.units;
-    const int head = seg / rq.groups, row0 = (seg % rq.groups) * S::kRows;
-    const int first = (int)(u - seg_a), last = (int)(min(u1, seg_b) - seg_a);   // units [first, last)
-    const int n_group_rows = min(rq.rows * p.G - row0, S::kRows);
-    const int seen0 = rq.kv - rq.rows;   // row j sees tokens <= seen0 + j
-    // ---- this warp's units: first + warp, + 8, ...
-    const int mine = (last - first - warp + kAttnWarps - 1) / kAttnWarps;
-    const int32_t* table = p.table + (size_t)r * p.max_blocks;
-    // Blocks of 32 of the warp's units at a time, one a lane.
-    int ids = 0;
-    float ks_l = 0.0f, vs_l = 0.0f;
-    auto look_up = [&](int i0) {
-      const int i = i0 + lane;
-      ids = -1;
-      if (i < mine) {
-        const int tok = (first + warp + i * kAttnWarps) * kUnit;
-        if (tok < rq.kv) {
-          const int b = table[tok / p.B];
-          if (b >= 0 && b < p.n_blocks) {
-            ids = b;
-            ks_l = p.k_scale[(size_t)b * p.K + head];
-            vs_l = p.v_scale[(size_t)b * p.K + head];
-          }
-        }
-      }
-    };
-    auto issue = [&](int i) {   // the whole warp; unit i of this warp into its stage
-      if ((i & 31) == 0) look_up(i);
-      const int b = __shfl_sync(0xffffffffu, ids, i & 31);
-      const float ks = __shfl_sync(0xffffffffu, ks_l, i & 31), vs = __shfl_sync(0xffffffffu, vs_l, i & 31);
-      const int s = (int)((phase_base + i) % S::kStages);
-      if (lane == 0) {
-        T.scales[warp][s] = b >= 0 ? make_float2(ks, vs) : make_float2(-1.0f, 0.0f);
-        const uint32_t bar = bar0 + 8 * s, dst = ring + s * S::kStage;
-        if (b >= 0) {
-          mbar_arrive_expect_tx(bar, S::kStage);
-          const int tok = ((first + warp + i * kAttnWarps) * kUnit) % p.B;
-#pragma unroll
-          for (int x = 0; x < S::kPanels; ++x) {
-            tma_load_4d(dst + x * kUnit * 128, &p.k, x * 128, tok, head, b, bar, pol);
-            tma_load_4d(dst + S::kSide + x * kUnit * 128, &p.v, x * 128, tok, head, b, bar, pol);
-          }
-        } else {
-          mbar_arrive(bar);
-        }
-      }
-      __syncwarp();
-    };
-    const int ahead = min(mine, S::kStages);
-    if (!dead)
-      for (int i = 0; i < ahead; ++i) issue(i);
+    return false;
+  };
 
-    // ---- queries to f16, a warp a row
-    for (int n = warp; n < S::kRows; n += kAttnWarps) {
+  // ---- copies: 32 of the warp's units (first + warp, + 8, ...) at a time, a block id a lane
+  int mine, ids;
+  auto token_of = [&](int i) { return (sg.first + warp + i * kAttnWarps) * kUnit; };
+  auto block_of = [&](int i) {
+    int b = -1;
+    if (i < mine && token_of(i) < sg.rq.kv) b = p.table[(size_t)sg.r * p.max_blocks + token_of(i) / p.B];
+    return b >= 0 && b < p.n_blocks ? b : -1;
+  };
+  auto issue = [&](int i) {   // the whole warp; unit i of this warp into its stage
+    if ((i & 31) == 0 && i > 0) ids = block_of(i + lane);
+    const int b = __shfl_sync(0xffffffffu, ids, i & 31);
+    const int s = (int)((phase_base + i) % S::kStages);
+    if (lane == 0) {
+      const uint32_t bar = bar0 + 8 * s, dst = ring + s * S::kStage;
+      if (b >= 0) {
+        mbar_arrive_expect_tx(bar, S::kStage);
+        const int tok = token_of(i) % p.B;
+#pragma unroll
+        for (int x = 0; x < S::kPanels; ++x) {
+          tma_load_4d(dst + x * kUnit * 128, &p.k, x * 128, tok, sg.head, b, bar, pol);
+          tma_load_4d(dst + S::kSide + x * kUnit * 128, &p.v, x * 128, tok, sg.head, b, bar, pol);
+        }
+      } else {
+        mbar_arrive(bar);
+      }
+    }
+    __syncwarp();
+  };
+  // scales of 32 units, one a lane; ks = -1: the block is not there
+  float2 sc_l = make_float2(-1.0f, 0.0f), sc_n = sc_l;
+  auto scales_of = [&](int b) {
+    if (b < 0) return make_float2(-1.0f, 0.0f);
+    const size_t at = (size_t)b * p.K + sg.head;
+    return make_float2(p.k_scale[at], p.v_scale[at]);
+  };
+  // A segment's start: its first copies, scales and this warp's query rows are
+  // asked for together; nothing here waits but the copies for the block ids.
+  uint16_t qx[NT][D / 32];
+  auto open_segment = [&]() {
+    mine = (sg.last - sg.first - warp + kAttnWarps - 1) / kAttnWarps;
+    ids = block_of(lane);
+    const int n_rows = min(sg.rq.rows * p.G - sg.row0, S::kRows);
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      const int n = warp + k * kAttnWarps;
+      if (n < n_rows) {
+        const int j = (sg.row0 + n) / p.G, h = sg.head * p.G + (sg.row0 + n) % p.G;
+        const uint16_t* src = p.q + (sg.rq.start + j) * p.q_row_stride + h * p.q_head_stride + lane;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) qx[k][i] = src[32 * i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) qx[k][i] = 0;
+      }
+    }
+    if (!dead) {
+      const int ahead = min(mine, S::kStages);
+      for (int i = 0; i < ahead; ++i) issue(i);
+    }
+    sc_l = scales_of(ids);
+  };
+  // The query rows to f16, each scaled by a power of two. `slot`: the NaN mask to clear.
+  auto store_queries = [&](int slot) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      const int n = warp + k * kAttnWarps;
       uint16_t* dst = reinterpret_cast<uint16_t*>(T.q + n * S::kQStride);
       float x[D / 32];
       float top = 0.0f;
-      if (n < n_group_rows) {
-        const int j = (row0 + n) / p.G, h = head * p.G + (row0 + n) % p.G;
-        const uint16_t* src = p.q + (rq.start + j) * p.q_row_stride + h * p.q_head_stride;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          x[i] = __uint_as_float((uint32_t)src[lane + 32 * i] << 16);
-          if (fabsf(x[i]) < INFINITY) top = fmaxf(top, fabsf(x[i]));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) x[i] = 0.0f;
+      for (int i = 0; i < D / 32; ++i) {
+        x[i] = __uint_as_float((uint32_t)qx[k][i] << 16);
+        if (fabsf(x[i]) < INFINITY) top = fmaxf(top, fabsf(x[i]));
       }
       top = warp_max(top);
       const int e = top > 0.0f ? min(max(floor_log2_abs(top), -100), 126) : 0;
+      const float f = exp2i(-e);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        dst[lane + 32 * i] = __half_as_ushort(__float2half_rn(ldexp_exact(x[i], -e)));
+      for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = __half_as_ushort(__float2half_rn(x[i] * f));
       if (lane == 0) T.q_scale[n] = p.scale * kLog2e * exp2i(e);
     }
-    for (int i = tid; i < D; i += kAttnThreads) T.nan_mask[i] = 0;
+    for (int i = tid; i < D; i += kAttnThreads) T.nan_mask[slot][i] = 0;
+  };
+
+  bool more = next_segment();
+  int turn = 0;
+  if (more) {
+    open_segment();
+    store_queries(0);
+  }
+  while (more) {
     __syncthreads();
+    const Segment cur = sg;
+    const Request& rq = cur.rq;
+    const int row0 = cur.row0, head = cur.head;
+    const int n_group_rows = min(rq.rows * p.G - row0, S::kRows);
+    const int seen0 = rq.kv - rq.rows;   // row j sees tokens <= seen0 + j
+    uint32_t* const nan_mask = T.nan_mask[turn];
 
     uint32_t qf[S::kQInRegs ? kMT : 1][S::kQInRegs ? NT : 1][2];
     const uint32_t q_at = smem_u32(T.q) + g * S::kQStride + t4 * 8;
@@ -371,8 +426,10 @@ attn_kernel(const __grid_constant__ AttnParams p) {
         }
         break;
       }
-      const float2 sc = T.scales[warp][s];
-      const int tok0 = (first + warp + i * kAttnWarps) * kUnit;
+      if ((i & 31) == 16) sc_n = scales_of(block_of((i & ~31) + 32 + lane));   // half a batch ahead
+      if ((i & 31) == 0 && i > 0) sc_l = sc_n;
+      const float2 sc = make_float2(__shfl_sync(0xffffffffu, sc_l.x, i & 31), __shfl_sync(0xffffffffu, sc_l.y, i & 31));
+      const int tok0 = token_of(i);
       if (sc.x != -1.0f) {
         const float vs = fminf(fmaxf(sc.y, 0x1p-60f), 0x1p60f);
         const float lvs = log2f(vs), rvs = 1.0f / vs;
@@ -438,7 +495,7 @@ attn_kernel(const __grid_constant__ AttnParams p) {
               for (int k = 0; k < 4; ++k)
                 if (((x >> (8 * k)) & 0x7Fu) == 0x7Fu) {
                   x &= ~(0xFFu << (8 * k));
-                  atomicOr(&T.nan_mask[byte + k], 1u << own);
+                  atomicOr(&nan_mask[byte + k], 1u << own);
                 }
             }
             asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(x) : "memory");
@@ -508,9 +565,13 @@ attn_kernel(const __grid_constant__ AttnParams p) {
       __syncwarp();
       if (i + S::kStages < mine) issue(i + S::kStages);
     }
-    phase_base += max(mine, 0);
+    phase_base += mine;
+    const int had = mine;
+    const int n_live = min(cur.last - cur.first, kAttnWarps);   // warps that had a unit
 
     // ---- the segment's end: join the warps' m, l, O
+    more = next_segment();
+    if (S::kOverlap && more) open_segment();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -522,21 +583,21 @@ attn_kernel(const __grid_constant__ AttnParams p) {
           T.l[warp][n * 8 + t4 * 2 + k] = l[n][k];
         }
       }
-    float* mine_o = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw))) + warp * (S::kRing / 4);
-    if (mine > 0) {
+    if (had > 0) {
+      float* const own = join + warp * kJoinStep;
 #pragma unroll
       for (int c = 0; c < kMT; ++c)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float2*>(mine_o + (n * 8 + t4 * 2 + k) * D + c * 16 + 2 * g) =
+            *reinterpret_cast<float2*>(own + (n * 8 + t4 * 2 + k) * D + c * 16 + 2 * g) =
                 make_float2(o[c][n][k], o[c][n][k + 2]);
     }
     __syncthreads();
-    const bool whole = seg_a >= u0 && seg_b <= u1;
-    const int slot = cta * 2 + (seg_a <= u0 ? 0 : 1);
-    const int n_live = min(last - first, kAttnWarps);   // warps that had a unit
+    const bool whole = cur.whole;
+    const int slot = cta * 2 + (cur.starts ? 1 : 0);
+    if (S::kOverlap && more) store_queries(turn ^ 1);
     for (int e = tid; e < n_group_rows * (D / 4); e += kAttnThreads) {
       const int n = e / (D / 4), d = (e % (D / 4)) * 4;
       float top = -INFINITY;
@@ -547,8 +608,7 @@ attn_kernel(const __grid_constant__ AttnParams p) {
         const float mw = T.m[w][n];
         // a warp whose every weight is NaN still has m = -inf and must show
         const float f = mw == top ? 1.0f : exp2_fast(mw - top);
-        const float4 b = *reinterpret_cast<const float4*>(
-            reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw))) + w * (S::kRing / 4) + n * D + d);
+        const float4 b = *reinterpret_cast<const float4*>(join + w * kJoinStep + n * D + d);
         sum = fmaf(T.l[w][n], f, sum);
         a.x = fmaf(b.x, f, a.x);
         a.y = fmaf(b.y, f, a.y);
@@ -557,10 +617,10 @@ attn_kernel(const __grid_constant__ AttnParams p) {
       }
       const int j = (row0 + n) / p.G, h = head * p.G + (row0 + n) % p.G;
       const uint32_t see = (2u << j) - 1u;
-      if (T.nan_mask[d] & see) a.x = NAN;
-      if (T.nan_mask[d + 1] & see) a.y = NAN;
-      if (T.nan_mask[d + 2] & see) a.z = NAN;
-      if (T.nan_mask[d + 3] & see) a.w = NAN;
+      if (nan_mask[d] & see) a.x = NAN;
+      if (nan_mask[d + 1] & see) a.y = NAN;
+      if (nan_mask[d + 2] & see) a.z = NAN;
+      if (nan_mask[d + 3] & see) a.w = NAN;
       if (whole) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
@@ -573,9 +633,13 @@ attn_kernel(const __grid_constant__ AttnParams p) {
         if (d == 0) p.part_ml[(size_t)slot * S::kRows + n] = make_float2(top, sum);
       }
     }
-    proxy_fence();   // O lay where TMA writes next
-    __syncthreads();
-    u = seg_a + last;
+    if (!S::kOverlap && more) {
+      proxy_fence();   // O lay where TMA writes next
+      __syncthreads();
+      open_segment();
+      store_queries(turn ^ 1);
+    }
+    turn ^= 1;
   }
   __syncthreads();
   if (tid == 0) p.failed[cta] = T.failed;
@@ -610,15 +674,14 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   const long long u1 = (c + 1) * line.share;
   if (u1 >= line.total) return;   // the last share: its segment ends in it
   const Request rq = request_of(p, line.r, kRows);
-  const int seg = (int)((u1 - 1 - line.base) / rq.units);
-  const long long seg_a = line.base + (long long)seg * rq.units, seg_b = seg_a + rq.units;
-  if (seg_a < u1 - line.share || seg_b <= u1) return;   // begins earlier, or ends here
+  const int len = p.lead + rq.units, seg = (int)((u1 - 1 - line.base) / len);
+  const long long seg_a = line.base + (long long)seg * len, seg_b = seg_a + len, first_unit = seg_a + p.lead;
+  if (first_unit < u1 - line.share || first_unit >= u1 || seg_b <= u1) return;   // starts elsewhere, or ends here
   const int pieces = (int)((seg_b - 1) / line.share) - c + 1;
   const int head = seg / rq.groups, row0 = (seg % rq.groups) * kRows;
   const int n = blockIdx.y;
   if (n >= min(rq.rows * p.G - row0, kRows)) return;
-  const int slot0 = c * 2 + (seg_a <= u1 - line.share ? 0 : 1);
-  auto slot_of = [&](int i) { return i == 0 ? slot0 : (c + i) * 2; };
+  auto slot_of = [&](int i) { return (c + i) * 2 + (i == 0 ? 1 : 0); };
   const int d4 = threadIdx.x % kLanes, at = threadIdx.x / kLanes;
   float top = -INFINITY;
   for (int i = 0; i < pieces; ++i) top = fmaxf(top, p.part_ml[(size_t)slot_of(i) * kRows + n].x);
@@ -671,12 +734,9 @@ int tiles_for(int D, int rows) {
 }
 
 template <int D, int NT>
-constexpr int attn_smem() { return Shape<D, NT>::kRing * kAttnWarps + (int)sizeof(Tail<D, NT>) + 1024; }
+constexpr int attn_smem() { return Shape<D, NT>::kWarpBytes * kAttnWarps + (int)sizeof(Tail<D, NT>) + 1024; }
 
-int ctas_per_sm(int D, int nt) {
-  const int ring = (nt > 3 ? (D == 64 && nt < 6 ? 6 : nt) : (D == 64 ? 6 : 3)) * 2 * kUnit * D * kAttnWarps;
-  return ring <= 100 * 1024 ? 2 : 1;
-}
+int ctas_per_sm(int D, int nt) { return nt * D <= 128 ? 2 : 1; }   // Shape::kCtas
 
 struct AttnLayout {
   size_t off_failed, off_ml, off_o, total;
@@ -818,6 +878,7 @@ int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_str
   p.part_o = reinterpret_cast<float*>(w + L.off_o);
   p.n_ctas = L.n_ctas;
   p.least = kAttnWarps;   // a unit for every warp
+  p.lead = 2048 / D;
   cudaStream_t st = as_stream(stream);
   cudaError_t e;
   if (D == 64) e = launch_attn_d<64>(L.nt, p, st);

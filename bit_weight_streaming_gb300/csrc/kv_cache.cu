@@ -1,6 +1,8 @@
 // The 8-bit key/value cache: block tables and slots from request lengths, and
 // the norm, rotation and E4M3 write of a step's queries, keys and values.
 // Contracts in include/bws.h.
+#include <atomic>
+
 #include "bws_abi_util.h"
 #include "bws_common.cuh"
 #include "bws_internal.h"
@@ -33,6 +35,7 @@ struct PlanParams {
   const int32_t* n_free;
   int n_rows;
   int32_t *slots, *positions, *row_start, *kv_lens, *n_free_out, *status;
+  int vec;   // slots and positions on 16-byte boundaries
 };
 
 // Largest r in [0, n) with a[r] <= i, a non-decreasing and a[0] = 0.
@@ -48,9 +51,10 @@ BWS_DEV int last_not_above(const int* a, int n, int i) {
 BWS_DEV int clamp_i32(long long v) { return v > 0x7fffffffLL ? 0x7fffffff : (int)v; }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
-  extern __shared__ int s_plan[];   // rows before [R + 1], then blocks before [R + 1]
+  extern __shared__ int s_plan[];   // rows before [R + 1], blocks before [R + 1], lengths [R]
   int* s_row = s_plan;
   int* s_blk = s_plan + p.R + 1;
+  int* s_seq = s_plan + 2 * (p.R + 1);
   __shared__ long long s_wr[kPlanThreads / 32], s_wb[kPlanThreads / 32];
   __shared__ int s_over;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -66,6 +70,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
     const long long seq = max(p.seq_lens[r], 0), nw = max(p.new_lens[r], 0);
     const long long have = (seq + p.B - 1) / p.B, need = (seq + nw + p.B - 1) / p.B;
     s_row[r] = (int)nw;
+    s_seq[r] = (int)seq;
     s_blk[r] = (int)(need - have);
     rows += nw;
     blks += need - have;
@@ -100,7 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
   if (blockIdx.x == 0) {
     for (int r = tid; r <= p.R; r += kPlanThreads) {
       p.row_start[r] = s_row[r];
-      if (r < p.R) p.kv_lens[r] = clamp_i32((long long)max(p.seq_lens[r], 0) + max(p.new_lens[r], 0));
+      if (r < p.R) p.kv_lens[r] = clamp_i32((long long)s_seq[r] + max(p.new_lens[r], 0));
     }
     if (tid == 0) {
       *p.n_free_out = max(n_free - taken, 0);
@@ -111,30 +116,56 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
   const int step = gridDim.x * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
   for (long long i = first; i < taken; i += step) {
     const int r = last_not_above(s_blk, p.R, (int)i);
-    const long long c = ((long long)max(p.seq_lens[r], 0) + p.B - 1) / p.B + (i - s_blk[r]);
+    const long long c = ((long long)s_seq[r] + p.B - 1) / p.B + (i - s_blk[r]);
     if (c < p.max_blocks) p.table[(size_t)r * p.max_blocks + c] = i < n_free ? p.free_blocks[n_free - 1 - i] : -1;
   }
-  for (long long t = first; t < p.n_rows; t += step) {
-    int slot = -1, pos = -1;
-    if (t < total) {
-      const int r = last_not_above(s_row, p.R, (int)t);
-      const int seq = max(p.seq_lens[r], 0);
-      const long long at = (long long)seq + (t - s_row[r]);
-      const long long c = at / p.B, have = ((long long)seq + p.B - 1) / p.B;
-      int blk = -1;
-      if (c < p.max_blocks) {
-        if (c < have) {
-          blk = p.table[(size_t)r * p.max_blocks + c];
-        } else {
-          const long long i = s_blk[r] + (c - have);
-          if (i < n_free) blk = p.free_blocks[n_free - 1 - i];
+  // Four rows a thread: B is a multiple of 16, so a thread whose rows belong to
+  // one request meets at most two blocks.
+  for (long long t0 = 4LL * first; t0 < p.n_rows; t0 += 4LL * step) {
+    int slot[4], pos[4];
+    int r = t0 < total ? last_not_above(s_row, p.R, (int)t0) : 0;
+    long long c_known = -1;
+    int blk = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long t = t0 + i;
+      slot[i] = pos[i] = -1;
+      if (t < total) {
+        if (t >= s_row[r + 1]) {   // the next request with rows
+          do ++r; while (t >= s_row[r + 1]);
+          c_known = -1;
         }
+        const int seq = s_seq[r];
+        const long long at = (long long)seq + (t - s_row[r]);
+        const long long c = at / p.B;
+        if (c != c_known) {
+          c_known = c;
+          blk = -1;
+          const long long have = ((long long)seq + p.B - 1) / p.B;
+          if (c < p.max_blocks) {
+            if (c < have) {
+              blk = p.table[(size_t)r * p.max_blocks + c];
+            } else {
+              const long long k = s_blk[r] + (c - have);
+              if (k < n_free) blk = p.free_blocks[n_free - 1 - k];
+            }
+          }
+        }
+        pos[i] = clamp_i32(at);
+        if (blk >= 0) slot[i] = clamp_i32((long long)blk * p.B + at % p.B);
       }
-      pos = clamp_i32(at);
-      if (blk >= 0) slot = clamp_i32((long long)blk * p.B + at % p.B);
     }
-    p.slots[t] = slot;
-    p.positions[t] = pos;
+    if (p.vec && t0 + 3 < p.n_rows) {
+      *reinterpret_cast<int4*>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t0 + i < p.n_rows) {
+          p.slots[t0 + i] = slot[i];
+          p.positions[t0 + i] = pos[i];
+        }
+    }
   }
 }
 
@@ -153,74 +184,87 @@ struct AppendParams {
   int stage_rows;    // rows of a run kept in shared memory between the two passes
 };
 
-BWS_DEV float bf16f(uint32_t v16) { return __uint_as_float(v16 << 16); }
+// A head is held eight values a lane by D / 8 neighbouring lanes ("group"), so
+// a warp works on 32 / (D / 8) rows at once and every load is 16 bytes.
+template <int D>
+struct Head {
+  static constexpr int kLanes = D / 8;
+  static constexpr int kRows = 32 / kLanes;
+};
 
-// A lane's E = D / 32 neighbouring values of one head.
-template <int E>
-BWS_DEV void load_head(const uint16_t* p, float (&x)[E]) {
-  uint32_t w[E / 2];
-  if constexpr (E == 2) {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else if constexpr (E == 4) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x; w[1] = v.y;
-  } else {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-  }
+BWS_DEV void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    x[2 * i] = bf16f(w[i] & 0xFFFFu);
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
 
-template <int E>
-BWS_DEV void norm_head(float (&x)[E], const float (&w)[E], float eps) {
+template <int D>
+BWS_DEV void norm_head(float (&x)[8], const float (&w)[8], float eps) {
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < E; ++i) s = fmaf(x[i], x[i], s);
-  s = warp_sum(s);
-  const float r = rsqrtf(s * (1.0f / (32 * E)) + eps);
+  for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
 #pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = x[i] * r * w[i];
+  for (int o = Head<D>::kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const float r = rsqrtf(s * (1.0f / D) + eps);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
 }
 
 // cos and sin of position * inv_freq[i] for a row's rot / 2 pairs, in turns:
 // f = inv_freq / 2 pi, and only the turn's fraction is kept. Below 2^24 the
-// position is exact in FP32 and f two FP32 parts (48 bits): the high product is
-// exact as a rounded product and its FMA remainder, so whole turns leave it
-// before the parts are added, without FP64 (which runs at about 2 a clock and
-// SM here). From 2^24 on the product is taken in FP64. Either way the fraction
-// is off by a few 2^-24.
-BWS_DEV void row_angles(int pos, const float* inv_freq, int half, float2* cs, int lane) {
-  const float fp = (float)pos;
-  const bool near = pos < (1 << 24) && pos > -(1 << 24);
-  for (int i = lane; i < half; i += 32) {
-    const double f = (double)inv_freq[i] * 0.15915494309189533577;
-    float t;
-    if (near) {
-      const float fh = (float)f, fl = (float)(f - (double)fh);
-      const float a = fh * fp, e = fmaf(fh, fp, -a);
-      t = (a - rintf(a)) + fmaf(fl, fp, e);
-      t -= rintf(t);
-    } else {
-      const double d = f * (double)pos;
-      t = (float)(d - rint(d));
-    }
-    float s, c;
-    sincospif(2.0f * t, &s, &c);
-    cs[i] = make_float2(c, s);
-  }
-}
+// position is exact in FP32 and f two FP32 parts (48 bits, formed once per
+// warp): the high product is exact as a rounded product and its FMA remainder,
+// so whole turns leave it before the parts are added, without FP64 (which runs
+// at about 2 a clock and SM here). From 2^24 on the product is taken in FP64.
+// Either way the fraction is off by a few 2^-24.
+template <int D>
+struct Angles {
+  static constexpr int kEach = D / 2 / Head<D>::kLanes;   // pairs a lane forms: sl + k * kLanes
+  float fh[kEach], fl[kEach];
 
-// Rotates a head held E values a lane; buf: the warp's own D floats.
-template <int E>
-BWS_DEV void rotate_head(float (&x)[E], const float2* cs, int rot, bool interleaved, float* buf, int lane) {
-  const int base = lane * E;
+  BWS_DEV void init(const float* inv_freq, int half, int sl) {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int i = sl + k * Head<D>::kLanes;
+      const double f = i < half ? (double)inv_freq[i] * 0.15915494309189533577 : 0.0;
+      fh[k] = (float)f;
+      fl[k] = (float)(f - (double)fh[k]);
+    }
+  }
+  BWS_DEV void form(int pos, const float* inv_freq, int half, int sl, float2* cs) const {
+    const float fp = (float)pos;
+    const bool near = pos < (1 << 24) && pos > -(1 << 24);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int i = sl + k * Head<D>::kLanes;
+      if (i >= half) break;
+      float t;
+      if (near) {
+        const float a = fh[k] * fp, e = fmaf(fh[k], fp, -a);
+        t = (a - rintf(a)) + fmaf(fl[k], fp, e);
+        t -= rintf(t);
+      } else {
+        const double d = (double)inv_freq[i] * 0.15915494309189533577 * (double)pos;
+        t = (float)(d - rint(d));
+      }
+      float s, c;
+      sincospif(2.0f * t, &s, &c);
+      cs[i] = make_float2(c, s);
+    }
+  }
+};
+
+// Rotates a head; cs: its row's angles, buf: the group's own D floats (used
+// where a pair's halves do not lie a whole number of lanes apart).
+template <int D>
+BWS_DEV void rotate_head(float (&x)[8], const float2* cs, int rot, bool interleaved, float* buf, int sl) {
+  const int base = sl * 8, half = rot >> 1;
   if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < E; i += 2) {
+    for (int i = 0; i < 8; i += 2) {
       if (base + i < rot) {
         const float2 a = cs[(base + i) >> 1];
         const float u = x[i], v = x[i + 1];
@@ -230,20 +274,29 @@ BWS_DEV void rotate_head(float (&x)[E], const float2* cs, int rot, bool interlea
     }
     return;
   }
-  __syncwarp();   // the last head's reads of buf are done
+  float y[8];
+  if ((half & 7) == 0) {
+    const int step = half >> 3;
+    const int from = base < half ? step : base < rot ? -step : 0;
 #pragma unroll
-  for (int i = 0; i < E; ++i) buf[base + i] = x[i];
-  __syncwarp();
-  const int half = rot >> 1;
+    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], (threadIdx.x & 31) + from);
+  } else {
+    __syncwarp();   // the last head's reads of buf are done
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
+    for (int i = 0; i < 8; ++i) buf[base + i] = x[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int d = base + i;
+      y[i] = d < half ? buf[d + half] : d < rot ? buf[d - half] : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
     const int d = base + i;
-    if (d < half) {
-      const float2 a = cs[d];
-      x[i] = x[i] * a.x - buf[d + half] * a.y;
-    } else if (d < rot) {
-      const float2 a = cs[d - half];
-      x[i] = x[i] * a.x + buf[d - half] * a.y;
+    if (d < rot) {
+      const float2 a = cs[d < half ? d : d - half];
+      x[i] = x[i] * a.x + y[i] * (d < half ? -a.y : a.y);
     }
   }
 }
@@ -256,70 +309,77 @@ BWS_DEV int scale_exponent(float amax) {
   return min(max(e, -60), 60);
 }
 
-template <int E>
-BWS_DEV void store_codes(uint8_t* p, const float (&x)[E], float inv) {
-  uint32_t h[E / 2];
+BWS_DEV void store_codes(uint8_t* p, const float (&x)[8], float inv) {
+  uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) h[i] = f32x2_to_e4m3x2(x[2 * i + 1] * inv, x[2 * i] * inv);
-  if constexpr (E == 2) {
-    *reinterpret_cast<uint16_t*>(p) = (uint16_t)h[0];
-  } else if constexpr (E == 4) {
-    *reinterpret_cast<uint32_t*>(p) = h[0] | (h[1] << 16);
-  } else {
-    *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-  }
+  for (int i = 0; i < 4; ++i) h[i] = f32x2_to_e4m3x2(x[2 * i + 1] * inv, x[2 * i] * inv);
+  *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// Query CTAs: a warp takes heads_per heads of one row, whose angles it forms
-// once. Key/value CTAs: one span of rows, one kv head, one side; each run of
-// rows that starts in the span is normed and rotated by the warps, a row each,
-// its largest magnitude joined over the CTA, and written under the scale that
+// Query warps take Head::kRows rows and heads_per heads of them, whose angles
+// they form once. Key/value CTAs: one span of rows, one kv head, one side; each
+// run of rows that starts in the span is normed and rotated by the warps, its
+// largest magnitude joined over the CTA, and written under the scale that
 // follows. Between the two passes the values wait in shared memory (the first
 // stage_rows rows; the rest, in long runs of wide heads, are formed again: the
-// rows are in L1 by then).
+// rows are in L1 by then). Every loop asks for its next rows before it works on
+// the ones it has.
 // Bound: launch and three dependent loads for a decoded token, the bytes of
 // the rows for a prompt chunk.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
-  constexpr int E = D / 32;
-  extern __shared__ float s_stage[];                 // [stage_rows][D]
-  __shared__ float s_buf[kAppendWarps][D];
-  __shared__ float2 s_cs[kAppendWarps][D / 2];
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
+  using Hd = Head<D>;
+  constexpr int kStep = kAppendWarps * Hd::kRows;   // rows of a key/value CTA's round
+  extern __shared__ __align__(16) float s_stage[];  // [stage_rows][D]
+  __shared__ __align__(16) float s_buf[kAppendWarps][Hd::kRows][D];
+  __shared__ __align__(16) float2 s_cs[kAppendWarps][Hd::kRows][D / 2];
   __shared__ float s_amax[kAppendWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane / Hd::kLanes, sl = lane % Hd::kLanes;
   const bws_qkv& in = p.in;
   const int half = in.rot >> 1;
+  float2* const cs = s_cs[warp][sub];
+  float* const buf = s_buf[warp][sub];
   pdl_launch_dependents();
   pdl_wait();
+  Angles<D> angles;
 
   if ((int)blockIdx.x >= p.n_kv_ctas) {
     const int groups = (in.n_q_heads + p.heads_per - 1) / p.heads_per;
     const long long unit = (long long)(blockIdx.x - p.n_kv_ctas) * kAppendWarps + warp;
-    const int row = (int)(unit / groups);
-    if (row >= in.n_rows) return;
+    const int row0 = (int)(unit / groups) * Hd::kRows, row = row0 + sub;
+    if (row0 >= in.n_rows) return;
+    const bool live = row < in.n_rows;
     const int h0 = (int)(unit % groups) * p.heads_per, h1 = min(h0 + p.heads_per, in.n_q_heads);
-    float w[E];
+    const uint16_t* src = in.q + (live ? row : row0) * in.q_row_stride + sl * 8;
+    uint4 raw = *reinterpret_cast<const uint4*>(src + h0 * in.q_head_stride);
+    float w[8];
     if (in.q_weight != nullptr) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) w[i] = in.q_weight[lane * E + i];
+      for (int i = 0; i < 8; ++i) w[i] = in.q_weight[sl * 8 + i];
     }
-    row_angles(in.positions[row], in.inv_freq, half, s_cs[warp], lane);
-    __syncwarp();
+    if (half > 0) {
+      const int pos = in.positions[live ? row : row0];
+      angles.init(in.inv_freq, half, sl);
+      angles.form(pos, in.inv_freq, half, sl, cs);
+      __syncwarp();
+    }
     for (int h = h0; h < h1; ++h) {
-      float x[E];
-      load_head<E>(in.q + row * in.q_row_stride + h * in.q_head_stride + lane * E, x);
-      if (in.q_weight != nullptr) norm_head<E>(x, w, in.eps);
-      rotate_head<E>(x, s_cs[warp], in.rot, in.interleaved != 0, s_buf[warp], lane);
-      uint32_t o[E / 2];
+      const uint4 now = raw;
+      if (h + 1 < h1) raw = *reinterpret_cast<const uint4*>(src + (h + 1) * in.q_head_stride);
+      float x[8];
+      unpack8(now, x);
+      if (in.q_weight != nullptr) norm_head<D>(x, w, in.eps);
+      if (half > 0) rotate_head<D>(x, cs, in.rot, in.interleaved != 0, buf, sl);
+      uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
         o[i] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      uint16_t* dst = p.q_out + ((size_t)row * in.n_q_heads + h) * D + lane * E;
-      if constexpr (E == 2) *reinterpret_cast<uint32_t*>(dst) = o[0];
-      else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
-      else *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (live)
+        *reinterpret_cast<uint4*>(p.q_out + ((size_t)row * in.n_q_heads + h) * D + sl * 8) =
+            make_uint4(o[0], o[1], o[2], o[3]);
     }
     return;
   }
@@ -329,61 +389,82 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int side = blockIdx.x & 1, head = (int)(blockIdx.x >> 1) % K;
   const int t0 = (int)((blockIdx.x >> 1) / K) * p.span, t1 = min(t0 + p.span, in.n_rows);
   const long long n_slots = (long long)c.n_blocks * B;
-  const uint16_t* src = side ? in.v + head * in.v_head_stride : in.k + head * in.k_head_stride;
   const long long row_stride = side ? in.v_row_stride : in.k_row_stride;
-  const bool normed = !side && in.k_weight != nullptr;
-  float w[E];
+  const uint16_t* src = (side ? in.v + head * in.v_head_stride : in.k + head * in.k_head_stride) + sl * 8;
+  const bool normed = !side && in.k_weight != nullptr, turned = !side && half > 0;
+  const int mine = warp * Hd::kRows + sub;   // this group's first row of a round
+  auto row_at = [&](int row) { return *reinterpret_cast<const uint4*>(src + min(row, in.n_rows - 1) * row_stride); };
+  auto pos_at = [&](int row) { return turned ? in.positions[min(row, in.n_rows - 1)] : 0; };
+  float w[8];
   if (normed) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) w[i] = in.k_weight[lane * E + i];
+    for (int i = 0; i < 8; ++i) w[i] = in.k_weight[sl * 8 + i];
   }
-
-  auto form = [&](int row, float (&x)[E]) {
-    load_head<E>(src + row * row_stride + lane * E, x);
-    if (side) return;
-    if (normed) norm_head<E>(x, w, in.eps);
-    if (half > 0) {
+  if (turned) angles.init(in.inv_freq, half, sl);
+  auto form = [&](const uint4& raw, int pos, float (&x)[8]) {
+    unpack8(raw, x);
+    if (normed) norm_head<D>(x, w, in.eps);
+    if (turned) {
       __syncwarp();
-      row_angles(in.positions[row], in.inv_freq, half, s_cs[warp], lane);
+      angles.form(pos, in.inv_freq, half, sl, cs);
       __syncwarp();
-      rotate_head<E>(x, s_cs[warp], in.rot, in.interleaved != 0, s_buf[warp], lane);
+      rotate_head<D>(x, cs, in.rot, in.interleaved != 0, buf, sl);
     }
   };
 
   int t = t0;
   while (t < t1) {
-    const int slot = in.slots[t];
+    // rows t - 1 .. t + 30's slots, a lane each; the first round's rows beside them
+    const int at = t - 1 + lane;
+    const int window = at >= 0 && at < in.n_rows ? in.slots[at] : -2;
+    uint4 raw = row_at(t + mine);
+    int pos = pos_at(t + mine);
+    const int before = __shfl_sync(0xffffffffu, window, 0), slot = __shfl_sync(0xffffffffu, window, 1);
     if (slot < 0 || slot >= n_slots) { ++t; continue; }
     const int off = slot % B, room = B - off;
-    if (off != 0 && t > 0 && in.slots[t - 1] == slot - 1) { ++t; continue; }   // inside an earlier run
-    int m = 1;   // the run's rows: slots go on by one, inside the block
-    while (m < room) {
-      const int i = m + lane;
-      const bool on = i < room && t + i < in.n_rows && in.slots[t + i] == slot + i;
-      const unsigned b = __ballot_sync(0xffffffffu, on);
-      const int n = b == 0xffffffffu ? 32 : __ffs(~b) - 1;
-      m += n;
-      if (n < 32) break;
-    }
-    float amax = 0.0f;
-    for (int i = warp; i < m; i += kAppendWarps) {
-      float x[E];
-      form(t + i, x);
-#pragma unroll
-      for (int k = 0; k < E; ++k) {
-        const float a = fabsf(x[k]);
-        if (a < INFINITY) amax = fmaxf(amax, a);   // NaN and infinity set no scale
+    if (off != 0 && before == slot - 1) { ++t; continue; }   // inside an earlier run
+    // the run's rows: slots go on by one, inside the block
+    const unsigned on = __ballot_sync(0xffffffffu, lane == 0 || (lane - 1 < room && window == slot + lane - 1));
+    int m = on == 0xffffffffu ? 31 : __ffs(~on) - 2;
+    if (m == 31) {
+      while (m < room) {
+        const int i = m + lane;
+        const bool more = i < room && t + i < in.n_rows && in.slots[t + i] == slot + i;
+        const unsigned b = __ballot_sync(0xffffffffu, more);
+        const int n = b == 0xffffffffu ? 32 : __ffs(~b) - 1;
+        m += n;
+        if (n < 32) break;
       }
-      if (i < p.stage_rows) {
+    }
+    const int block = slot / B;
+    float* scale_at = (side ? c.v_scale : c.k_scale) + (size_t)block * K + head;
+    const float old = *scale_at;
+    float amax = 0.0f;
+    for (int i0 = 0; i0 < m; i0 += kStep) {
+      const int i = i0 + mine;
+      const uint4 now = raw;
+      const int here = pos;
+      if (i0 + kStep < m) {
+        raw = row_at(t + i + kStep);
+        pos = pos_at(t + i + kStep);
+      }
+      float x[8];
+      form(now, here, x);
+      if (i < m) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) s_stage[i * D + lane * E + k] = x[k];
+        for (int k = 0; k < 8; ++k) {
+          const float a = fabsf(x[k]);
+          if (a < INFINITY) amax = fmaxf(amax, a);   // NaN and infinity set no scale
+        }
+        if (i < p.stage_rows) {
+          float4* st = reinterpret_cast<float4*>(s_stage + i * D + sl * 8);
+          st[0] = make_float4(x[0], x[1], x[2], x[3]);
+          st[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
       }
     }
     amax = warp_max(amax);
     if (lane == 0) s_amax[warp] = amax;
-    const int block = slot / B;
-    float* scale_at = (side ? c.v_scale : c.k_scale) + (size_t)block * K + head;
-    const float old = *scale_at;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kAppendWarps; ++i) amax = fmaxf(amax, s_amax[i]);
@@ -402,15 +483,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
         w32[i] = f32x2_to_e4m3x2(a.y * f, a.x * f) | (f32x2_to_e4m3x2(b.y * f, b.x * f) << 16);
       }
     }
-    for (int i = warp; i < m; i += kAppendWarps) {
-      float x[E];
-      if (i < p.stage_rows) {
-#pragma unroll
-        for (int k = 0; k < E; ++k) x[k] = s_stage[i * D + lane * E + k];
+    uint8_t* dst = codes + (size_t)off * D + sl * 8;
+    for (int i0 = 0; i0 < m; i0 += kStep) {
+      const int i = i0 + mine;
+      float x[8];
+      if (i0 + kStep <= p.stage_rows || m <= p.stage_rows) {   // the same for the whole warp
+        if (i >= m) continue;
+        const float4* st = reinterpret_cast<const float4*>(s_stage + i * D + sl * 8);
+        const float4 a = st[0], b = st[1];
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
       } else {
-        form(t + i, x);
+        form(row_at(t + i), pos_at(t + i), x);
       }
-      store_codes<E>(codes + (size_t)(off + i) * D + lane * E, x, inv);
+      if (i < m) store_codes(dst + (size_t)i * D, x, inv);
     }
     __syncthreads();   // every thread has read the old scale and s_amax
     if (threadIdx.x == 0) *scale_at = scale;
@@ -486,12 +572,16 @@ int bws_kv_plan(const int32_t* seq_lens, const int32_t* new_lens, int n_requests
   for (const void* q : ptrs)
     if (!aligned(q, 4)) return fail(BWS_ERR_MISALIGNED, "%s: 4-byte alignment needed", name);
   PlanParams p = {seq_lens, new_lens, n_requests, block_tokens, block_table, max_blocks, free_blocks, n_free, n_rows,
-                  slots, positions, row_start, kv_lens, n_free_out, status};
+                  slots, positions, row_start, kv_lens, n_free_out, status,
+                  aligned(slots, 16) && aligned(positions, 16)};
+  static std::atomic<unsigned long long> attr{0};
+  const cudaError_t e = set_smem_once(attr, plan_kernel, (int)sizeof(int) * (3 * kPlanMaxRequests + 2));
+  if (e != cudaSuccess) return cuda_status(e, name);
   // four rows a thread, up to two CTAs an SM
   const long long want = ((long long)n_rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
   const long long most = 2LL * num_sms();
   const unsigned grid = (unsigned)(want < 1 ? 1 : want > most ? most : want);
-  return cuda_status(launch_pdl(plan_kernel, grid, kPlanThreads, 2 * sizeof(int) * ((size_t)n_requests + 1),
+  return cuda_status(launch_pdl(plan_kernel, grid, kPlanThreads, sizeof(int) * (3 * (size_t)n_requests + 2),
                                 as_stream(stream), p), name);
 }
 
@@ -527,20 +617,21 @@ int bws_qk_norm_rope_append(const bws_qkv* in, const bws_kv_cache* cache, uint16
   p.q_out = q_out;
   const long long sms = num_sms();
   // A span of one row gives every row of a decode batch its own CTA; longer
-  // calls take whole blocks, so that no CTA is launched only to find that its
-  // rows belong to an earlier run.
+  // calls take more, up to a block, so that few CTAs are launched only to find
+  // that their rows belong to an earlier run.
   const long long rows = in->n_rows;
-  long long span = rows * K * 2 / (sms * 16);
+  long long span = rows * K * 2 / (sms * 8);
   span = span < 1 ? 1 : span > cache->block_tokens ? cache->block_tokens : span;
   p.span = (int)span;
   const long long spans = (rows + span - 1) / span;
   const long long kv_ctas = spans * K * 2;
-  // heads of a row that share a warp's angles, as long as every SM keeps 16 warps
-  long long per = rows * H / (sms * 16);
+  // heads of a row that share a warp's angles, as long as every SM keeps 8 warps
+  const long long row_groups = (rows + 256 / D - 1) / (256 / D);
+  long long per = row_groups * H / (sms * 8);
   per = per < 1 ? 1 : per > 8 ? 8 : per;
   p.heads_per = (int)per;
   const long long groups = (H + per - 1) / per;
-  const long long q_ctas = (rows * groups + kAppendWarps - 1) / kAppendWarps;
+  const long long q_ctas = (row_groups * groups + kAppendWarps - 1) / kAppendWarps;
   if (kv_ctas + q_ctas >= (1LL << 31)) return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: too many rows", name);
   p.n_kv_ctas = (int)kv_ctas;
   long long stage = 32 * 1024 / (4 * D);

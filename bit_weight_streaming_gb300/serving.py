@@ -8,7 +8,7 @@ import ctypes as C
 import torch
 
 from ._lib import BwsError, check, lib
-from .api import _ptr, _stream, _ws
+from .api import _ws
 
 
 class _KvCache(C.Structure):
@@ -29,19 +29,34 @@ class _Qkv(C.Structure):
                 ("inv_freq", C.c_void_p), ("rot", C.c_int), ("interleaved", C.c_int), ("eps", C.c_float)]
 
 
-def _check(name, t, dtype, shape=None):
-    """A contiguous CUDA tensor of `dtype` (and of `shape`, None = any size)."""
-    if t is None or not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
-        raise BwsError(f"{name} must be a contiguous CUDA tensor of {dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
-        raise BwsError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+# The current stream's handle from a device index, without the stream object
+# torch.cuda.current_stream builds (2 us of a call's 10).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+_I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
 
 
-def _check_heads(name, t, dim, rows=None):
-    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1:
-        raise BwsError(f"{name} must be a CUDA bfloat16 tensor [rows, heads, {dim}] with a contiguous last dimension")
-    if rows is not None and t.shape[0] != rows:
-        raise BwsError(f"{name} has {t.shape[0]} rows, expected {rows}")
+def _check(name, t, dtype, shape):
+    """A contiguous CUDA tensor of `dtype` and `shape`."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise BwsError(f"{name} must be a contiguous CUDA tensor of {dtype}, shape {tuple(shape)}; it is {t.dtype}, "
+                       f"{tuple(t.shape)} on {t.device}")
+
+
+def _check_heads(name, t, rows, heads, dim):
+    if t.dtype is not _BF16 or t.shape != (rows, heads, dim) or not t.is_cuda:
+        raise BwsError(f"{name} must be a CUDA bfloat16 tensor [{rows}, {heads}, {dim}]; it is {t.dtype}, "
+                       f"{tuple(t.shape)} on {t.device}")
+    row, head, one = t.stride()
+    if one != 1:
+        raise BwsError(f"{name} must be contiguous in its last dimension")
+    return row, head
+
+
+def _fail(rc, what):
+    if rc:
+        check(rc, what)
 
 
 class KvCache:
@@ -52,15 +67,15 @@ class KvCache:
     [n_blocks, kv_heads]. The tensors stay the caller's."""
 
     def __init__(self, k, v, k_scale, v_scale):
-        if k.dtype != torch.uint8 or v.dtype != torch.uint8 or k.dim() != 4 or k.shape != v.shape or not k.is_cuda \
+        if k.dtype != _U8 or v.dtype != _U8 or k.dim() != 4 or k.shape != v.shape or not k.is_cuda \
                 or not v.is_cuda or k.stride() != v.stride():
             raise BwsError("k and v must be CUDA uint8 tensors [n_blocks, kv_heads, block_tokens, head_dim] of one "
                            "shape and one set of strides")
         n, h, b, d = k.shape
         if k.stride(3) != 1 or k.stride(2) != d:
             raise BwsError("the tokens of a (block, head) must be contiguous rows")
-        _check("k_scale", k_scale, torch.float32, (n, h))
-        _check("v_scale", v_scale, torch.float32, (n, h))
+        _check("k_scale", k_scale, _F32, (n, h))
+        _check("v_scale", v_scale, _F32, (n, h))
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_blocks, self.kv_heads, self.block_tokens, self.head_dim = n, h, b, d
         # a dimension of one entry has no stride of its own
@@ -69,6 +84,7 @@ class KvCache:
         self._struct = _KvCache(n, h, b, d, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                 block, head)
         self._at = C.addressof(self._struct)
+        self._attn_ws = {}      # workspace bytes by (query heads, rows)
 
     @classmethod
     def empty(cls, n_blocks, kv_heads, head_dim, block_tokens=64, device="cuda"):
@@ -92,26 +108,26 @@ def kv_plan(seq_lens, new_lens, block_tokens, block_table, free_blocks, n_free, 
     tokens need, from the end of free_blocks[:n_free]. Returns KvPlan(slots
     [n_rows], positions [n_rows], row_start [requests + 1], kv_lens
     [requests], n_free [1], status [1]: bits of bws_kv_plan_status)."""
-    R = seq_lens.shape[0]
-    i32 = torch.int32
-    _check("seq_lens", seq_lens, i32, (R,))
-    _check("new_lens", new_lens, i32, (R,))
-    _check("block_table", block_table, i32, (R, None))
-    _check("free_blocks", free_blocks, i32, (None,))
-    _check("n_free", n_free, i32, (1,))
+    R, wide = block_table.shape
+    one = (R,)
+    _check("seq_lens", seq_lens, _I32, one)
+    _check("new_lens", new_lens, _I32, one)
+    _check("block_table", block_table, _I32, (R, wide))
+    _check("free_blocks", free_blocks, _I32, (free_blocks.numel(),))
+    _check("n_free", n_free, _I32, (1,))
     if n_rows < 0:
         raise BwsError("n_rows must not be negative")
     # one allocation; each part starts on a 16-byte boundary
     a, b = (n_rows + 3) & ~3, (R + 4) & ~3
-    buf = torch.empty(2 * a + 2 * b + 8, dtype=i32, device=seq_lens.device)
+    buf = torch.empty(2 * a + 2 * b + 8, dtype=_I32, device=seq_lens.device)
     at = buf.data_ptr()
-    out = KvPlan(buf[:n_rows], buf[a:a + n_rows], buf[2 * a:2 * a + R + 1], buf[2 * a + b:2 * a + b + R],
-                 buf[2 * a + 2 * b:2 * a + 2 * b + 1], buf[2 * a + 2 * b + 4:2 * a + 2 * b + 5])
-    check(lib().bws_kv_plan(seq_lens.data_ptr(), new_lens.data_ptr(), R, block_tokens, block_table.data_ptr(),
-                            block_table.shape[1], free_blocks.data_ptr(), n_free.data_ptr(), n_rows, at, at + 4 * a,
-                            at + 8 * a, at + 8 * a + 4 * b, at + 8 * (a + b), at + 8 * (a + b) + 16,
-                            _stream(seq_lens.device)), "bws_kv_plan")
-    return out
+    _fail(lib().bws_kv_plan(seq_lens.data_ptr(), new_lens.data_ptr(), R, block_tokens, block_table.data_ptr(), wide,
+                            free_blocks.data_ptr(), n_free.data_ptr(), n_rows, at, at + 4 * a, at + 8 * a,
+                            at + 8 * a + 4 * b, at + 8 * (a + b), at + 8 * (a + b) + 16,
+                            _raw_stream(seq_lens.get_device())), "bws_kv_plan")
+    slots, _, positions, _, row_start, _, kv_lens, _, n_out, _, status, _ = buf.split(
+        (n_rows, a - n_rows, n_rows, a - n_rows, R + 1, b - R - 1, R, b - R, 1, 3, 1, 3))
+    return KvPlan(slots, positions, row_start, kv_lens, n_out, status)
 
 
 def qk_norm_rope_append(q, k, v, positions, slots, cache, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -122,26 +138,32 @@ def qk_norm_rope_append(q, k, v, positions, slots, cache, inv_freq=None, q_weigh
     fp32 [rot / 2] or None (no rotation). Returns the queries, bf16 [rows,
     q_heads, dim]; the cache changes in place."""
     T, H, D = q.shape
-    _check_heads("q", q, cache.head_dim)
-    _check_heads("k", k, cache.head_dim, T)
-    _check_heads("v", v, cache.head_dim, T)
-    if k.shape[1] != cache.kv_heads or v.shape[1] != cache.kv_heads:
-        raise BwsError(f"k and v must have the cache's {cache.kv_heads} heads")
-    _check("positions", positions, torch.int32, (T,))
-    _check("slots", slots, torch.int32, (T,))
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check(name, w, torch.float32, (D,))
+    K = cache.kv_heads
+    q_row, q_head = _check_heads("q", q, T, H, cache.head_dim)
+    k_row, k_head = _check_heads("k", k, T, K, D)
+    v_row, v_head = _check_heads("v", v, T, K, D)
+    one = (T,)
+    _check("positions", positions, _I32, one)
+    _check("slots", slots, _I32, one)
+    qw = kw = f = None
+    rot = 0
+    if q_weight is not None:
+        _check("q_weight", q_weight, _F32, (D,))
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _check("k_weight", k_weight, _F32, (D,))
+        kw = k_weight.data_ptr()
     if inv_freq is not None:
-        _check("inv_freq", inv_freq, torch.float32, (None,))
+        rot = 2 * inv_freq.numel()
+        _check("inv_freq", inv_freq, _F32, (rot // 2,))
+        f = inv_freq.data_ptr()
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty((T, H, D), dtype=_BF16, device=q.device)
     else:
-        _check("q_out", q_out, torch.bfloat16, (T, H, D))
-    a = _Qkv(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-             v.stride(1), T, H, positions.data_ptr(), slots.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
-             0 if inv_freq is None else 2 * inv_freq.shape[0], int(interleaved), eps)
-    check(lib().bws_qk_norm_rope_append(C.addressof(a), cache._at, q_out.data_ptr(), _stream(q.device)),
+        _check("q_out", q_out, _BF16, (T, H, D))
+    a = _Qkv(q.data_ptr(), q_row, q_head, k.data_ptr(), k_row, k_head, v.data_ptr(), v_row, v_head, T, H,
+             positions.data_ptr(), slots.data_ptr(), qw, kw, f, rot, interleaved, eps)
+    _fail(lib().bws_qk_norm_rope_append(C.addressof(a), cache._at, q_out.data_ptr(), _raw_stream(q.get_device())),
           "bws_qk_norm_rope_append")
     return q_out
 
@@ -158,27 +180,33 @@ def kv_attention(q, cache, block_table, row_start, kv_lens, max_rows, scale=None
     to dim ** -0.5. Returns out bf16 [rows, q_heads, dim], and with lse=True
     also the fp32 [rows, q_heads] log-sum-exp of the scores."""
     T, H, D = q.shape
-    _check_heads("q", q, cache.head_dim)
-    R = kv_lens.shape[0]
-    _check("block_table", block_table, torch.int32, (R, None))
-    _check("row_start", row_start, torch.int32, (R + 1,))
-    _check("kv_lens", kv_lens, torch.int32, (R,))
+    row, head = _check_heads("q", q, T, H, cache.head_dim)
+    R, wide = block_table.shape
+    _check("block_table", block_table, _I32, (R, wide))
+    _check("row_start", row_start, _I32, (R + 1,))
+    _check("kv_lens", kv_lens, _I32, (R,))
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((T, H, D), dtype=_BF16, device=q.device)
     else:
-        _check("out", out, torch.bfloat16, (T, H, D))
-    if lse is True:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    elif lse is not False:
-        _check("lse", lse, torch.float32, (T, H))
-    L = lib()
-    buf = _ws(ws, L.bws_kv_attention_workspace_size(H, cache.kv_heads, D, max_rows), q.device)
-    check(L.bws_kv_attention(q.data_ptr(), q.stride(0), q.stride(1), T, H, cache._at, block_table.data_ptr(),
-                             block_table.shape[1], R, row_start.data_ptr(), kv_lens.data_ptr(), max_rows,
-                             D ** -0.5 if scale is None else scale, out.data_ptr(),
-                             None if lse is False else lse.data_ptr(), buf.data_ptr(), buf.numel(),
-                             _stream(q.device)), "bws_kv_attention")
-    return out if lse is False else (out, lse)
+        _check("out", out, _BF16, (T, H, D))
+    if lse is False:
+        lse_at = None
+    else:
+        if lse is True:
+            lse = torch.empty((T, H), dtype=_F32, device=q.device)
+        else:
+            _check("lse", lse, _F32, (T, H))
+        lse_at = lse.data_ptr()
+    so = lib()
+    size = cache._attn_ws.get((H, max_rows))
+    if size is None:
+        size = cache._attn_ws[H, max_rows] = kv_attention_workspace_size(H, cache.kv_heads, D, max_rows)
+    buf = _ws(ws, size, q.device)
+    _fail(so.bws_kv_attention(q.data_ptr(), row, head, T, H, cache._at, block_table.data_ptr(), wide, R,
+                              row_start.data_ptr(), kv_lens.data_ptr(), max_rows, D ** -0.5 if scale is None else scale,
+                              out.data_ptr(), lse_at, buf.data_ptr(), buf.numel(), _raw_stream(q.get_device())),
+          "bws_kv_attention")
+    return out if lse_at is None else (out, lse)
 
 
 def draft_verify(target, tokens, row_start, accept_u, sample_u, max_rows, draft=None):
@@ -191,18 +219,24 @@ def draft_verify(target, tokens, row_start, accept_u, sample_u, max_rows, draft=
     then -1; n_out int32 [requests])."""
     T, V = target.shape
     R = sample_u.shape[0]
-    for name, t in (("target", target), ("draft", draft)):
-        if t is not None and (not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != (T, V)
-                              or (t.stride(1) != 1 and V > 1)):
-            raise BwsError(f"{name} must be a CUDA fp32 tensor [{T}, {V}] with a contiguous last dimension")
-    _check("tokens", tokens, torch.int32, (T,))
-    _check("accept_u", accept_u, torch.float32, (T,))
-    _check("sample_u", sample_u, torch.float32, (R,))
-    _check("row_start", row_start, torch.int32, (R + 1,))
-    out = torch.empty((R, max_rows), dtype=torch.int32, device=target.device)
-    n_out = torch.empty((R,), dtype=torch.int32, device=target.device)
-    check(lib().bws_draft_verify(target.data_ptr(), max(target.stride(0), V), _ptr(draft),
-                                 max(draft.stride(0), V) if draft is not None else 0, tokens.data_ptr(), T, V,
-                                 row_start.data_ptr(), R, accept_u.data_ptr(), sample_u.data_ptr(), max_rows,
-                                 out.data_ptr(), n_out.data_ptr(), _stream(target.device)), "bws_draft_verify")
-    return out, n_out
+    strides = [0, 0]
+    for i, t in enumerate((target, draft)):
+        if t is not None:
+            if t.dtype is not _F32 or t.shape != (T, V) or not t.is_cuda or (t.stride(1) != 1 and V > 1):
+                raise BwsError(f"target and draft must be CUDA fp32 tensors [{T}, {V}] with a contiguous last dimension")
+            strides[i] = max(t.stride(0), V)    # one row has no stride of its own
+    rows = (T,)
+    _check("tokens", tokens, _I32, rows)
+    _check("accept_u", accept_u, _F32, rows)
+    _check("sample_u", sample_u, _F32, (R,))
+    _check("row_start", row_start, _I32, (R + 1,))
+    if max_rows < 1:
+        raise BwsError("max_rows must be positive")
+    buf = torch.empty((R * (max_rows + 1),), dtype=_I32, device=target.device)
+    out, n_out = buf.split((R * max_rows, R))
+    at = buf.data_ptr()
+    _fail(lib().bws_draft_verify(target.data_ptr(), strides[0], None if draft is None else draft.data_ptr(), strides[1],
+                                 tokens.data_ptr(), T, V, row_start.data_ptr(), R, accept_u.data_ptr(),
+                                 sample_u.data_ptr(), max_rows, at, at + 4 * R * max_rows,
+                                 _raw_stream(target.get_device())), "bws_draft_verify")
+    return out.view(R, max_rows), n_out
