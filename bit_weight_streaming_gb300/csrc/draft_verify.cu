@@ -8,10 +8,9 @@
 // sends its sum to every CTA over distributed shared memory. CTA 0 finds the
 // range in which the running sum passes u * total and reads only that one again
 // (now in L2), first by sixteenths, a warp each, then word by word.
-// A lane adds FP32 numbers in two words (the rounded sum and what the rounding
-// left), which carries 48 bits: on this GPU FP64 adds run at a small fraction
-// of the FP32 rate and would set the time (1.3 FP64 adds per 4-byte word
-// against the HBM rate); FP64 takes over at the warp's 32 sums.
+// A warp adds FP32 numbers in two words (the rounded sum and what the rounding
+// left), which carries 48 bits: FP64 adds run at about 2 a clock and SM here and
+// would set the time. FP64 takes over at the warps' sums, in one warp.
 // Bound: the chain of dependent loads, the cluster's two barriers and the
 // launch for few requests; the bytes of one or two rows a request for many.
 #include <cooperative_groups.h>
@@ -71,20 +70,40 @@ BWS_DEV float weight_at(const Row& row, int v) {
 
 BWS_DEV float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
+// hi + lo += b's two words
+BWS_DEV void two_word_join(float& hi, float& lo, float bh, float bl) {
+  const float s = __fadd_rn(hi, bh);
+  const float b = __fsub_rn(s, hi);
+  const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(bh, b));
+  lo = __fadd_rn(__fadd_rn(lo, bl), e);
+  hi = s;
+}
+
 // Sum of w over [a, b) by one warp (the same in every lane). a % 4 == 0.
 template <bool VEC, bool HAS_Q>
 BWS_DEV double range_sum(const Row& row, int a, int b, int lane) {
   float hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
   if constexpr (VEC) {
     constexpr int U = 4;   // loads in flight: U rows of 512 bytes from p, and from q
-    int v = a + lane * 4;
-    for (; v + (U - 1) * 128 + 3 < b; v += U * 128) {
+    for (int v = a + lane * 4; v < b; v += U * 128) {
       float4 x[U], y[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        x[u] = load4(row.p + v + u * 128);
-        if constexpr (HAS_Q) y[u] = load4(row.q + v + u * 128);
-        else y[u] = make_float4(0, 0, 0, 0);
+        const int at = v + u * 128;
+        x[u] = y[u] = make_float4(0, 0, 0, 0);
+        if (at + 3 < b) {
+          x[u] = load4(row.p + at);
+          if constexpr (HAS_Q) y[u] = load4(row.q + at);
+        } else if (at < b) {   // the vocabulary's last words; a row may end with them
+          x[u].x = __ldg(row.p + at);
+          if (at + 1 < b) x[u].y = __ldg(row.p + at + 1);
+          if (at + 2 < b) x[u].z = __ldg(row.p + at + 2);
+          if constexpr (HAS_Q) {
+            y[u].x = __ldg(row.q + at);
+            if (at + 1 < b) y[u].y = __ldg(row.q + at + 1);
+            if (at + 2 < b) y[u].z = __ldg(row.q + at + 2);
+          }
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -95,32 +114,30 @@ BWS_DEV double range_sum(const Row& row, int a, int b, int lane) {
         two_word_add(hi[3], lo[3], d == 3 ? 0.0f : weight_of(x[u].w, y[u].w));
       }
     }
-    for (; v < b; v += 128) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (v + k < b) two_word_add(hi[k], lo[k], weight_at(row, v + k));
-    }
   } else {
-    int v = a + lane;
-    for (; v + 7 * 32 < b; v += 256) {
+    for (int v = a + lane; v < b; v += 256) {
       float x[8], y[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        x[u] = __ldg(row.p + v + u * 32);
-        y[u] = HAS_Q ? __ldg(row.q + v + u * 32) : 0.0f;
+        x[u] = y[u] = 0.0f;
+        if (v + u * 32 < b) {
+          x[u] = __ldg(row.p + v + u * 32);
+          if constexpr (HAS_Q) y[u] = __ldg(row.q + v + u * 32);
+        }
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u)
         two_word_add(hi[u & 3], lo[u & 3], v + u * 32 == row.certain ? 0.0f : weight_of(x[u], y[u]));
     }
-    for (; v < b; v += 32) two_word_add(hi[0], lo[0], weight_at(row, v));
   }
-  double s = 0.0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) s += (double)hi[k] + (double)lo[k];
+  for (int k = 1; k < 4; ++k) two_word_join(hi[0], lo[0], hi[k], lo[k]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float h = __shfl_xor_sync(0xffffffffu, hi[0], o), l = __shfl_xor_sync(0xffffffffu, lo[0], o);
+    two_word_join(hi[0], lo[0], h, l);
+  }
+  return (double)hi[0] + (double)lo[0];
 }
 
 BWS_DEV double warp_scan(double x, int lane) {
@@ -176,7 +193,8 @@ BWS_DEV int pick_range(const double* sums, int n, F target, double* before, int 
 
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p) {
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ double s_sum[kVerifyMaxCluster * kVerifyWarps], s_part[kVerifyWarps];
+  __shared__ double s_sum[kVerifyMaxCluster * kVerifyWarps], s_part[kVerifyWarps], s_left;
+  __shared__ int s_pick;
   __shared__ int s_stand;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -232,7 +250,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     cluster.sync();
     if (row.q == nullptr && row.certain < 0) break;
     bool any = false;   // is anything left of the target?
-    for (int i = lane; i < n_warps; i += 32) any |= s_sum[i] > 0.0;
+    for (int i = lane; i < n_warps; i += 32) any |= __double_as_longlong(s_sum[i]) > 0;
     if (__any_sync(0xffffffffu, any)) break;
     row.q = nullptr;
     row.certain = -1;
@@ -241,10 +259,20 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
   if (rank != 0) return;
 
   // ---- CTA 0: the range in which the running sum passes u * total ...
-  double before, t;
-  int k = pick_range(s_sum, n_warps, [&](double total) { return t = (double)p.sample_u[r] * total; }, &before, lane);
+  // (one warp: FP64 runs at about 2 a clock and SM)
+  if (warp == 0) {
+    double t, before;
+    const int k = pick_range(s_sum, n_warps, [&](double total) { return t = (double)p.sample_u[r] * total; }, &before, lane);
+    if (lane == 0) {
+      s_pick = k;
+      s_left = t - before;
+    }
+  }
+  __syncthreads();
+  const int k = s_pick;
+  const double left = s_left;
   int drawn = -1;
-  if (k >= 0) {   // the same in every warp
+  if (k >= 0) {
     // ... its sixteenths, a warp each, and the one in which it passes
     const int a = range_begin(k), b = range_begin(k + 1);
     const int part = ((b - a + 4 * kVerifyWarps - 1) / (4 * kVerifyWarps)) * 4;
@@ -254,12 +282,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     __syncthreads();
     if (warp != 0) return;
     double before1;
-    const int k1 = pick_range(s_part, kVerifyWarps, [&](double) { return t - before; }, &before1, lane);
+    const int k1 = pick_range(s_part, kVerifyWarps, [&](double) { return left; }, &before1, lane);
     // ... and the word
     if (k1 >= 0) {
       const int a2 = min(a + k1 * part, b), b2 = min(a2 + part, b);
       double base = before1;
-      const double left = t - before;
       int fallback = -1;
       for (int v0 = a2; v0 < b2 && drawn < 0; v0 += 128) {
         const int v = v0 + lane * 4;

@@ -48,6 +48,9 @@ BWS_DEV int last_not_above(const int* a, int n, int i) {
   return lo;
 }
 
+// Blocks that hold n tokens; n may be the sum of two lengths, below 2^32 - B.
+BWS_DEV uint32_t blocks_of(uint32_t n, int B) { return n / (uint32_t)B + (n % (uint32_t)B != 0 ? 1u : 0u); }
+
 BWS_DEV int clamp_i32(long long v) { return v > 0x7fffffffLL ? 0x7fffffff : (int)v; }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
@@ -67,14 +70,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
   long long rows = 0, blks = 0;
   bool over = false;
   for (int r = r0; r < r1; ++r) {
-    const long long seq = max(p.seq_lens[r], 0), nw = max(p.new_lens[r], 0);
-    const long long have = (seq + p.B - 1) / p.B, need = (seq + nw + p.B - 1) / p.B;
+    const uint32_t seq = max(p.seq_lens[r], 0), nw = max(p.new_lens[r], 0);
+    const uint32_t have = blocks_of(seq, p.B), need = blocks_of(seq + nw, p.B);
     s_row[r] = (int)nw;
     s_seq[r] = (int)seq;
     s_blk[r] = (int)(need - have);
     rows += nw;
     blks += need - have;
-    over |= need > p.max_blocks;
+    over |= need > (uint32_t)p.max_blocks;
   }
   long long ir = rows, ib = blks;
 #pragma unroll
@@ -116,7 +119,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
   const int step = gridDim.x * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
   for (long long i = first; i < taken; i += step) {
     const int r = last_not_above(s_blk, p.R, (int)i);
-    const long long c = ((long long)s_seq[r] + p.B - 1) / p.B + (i - s_blk[r]);
+    const long long c = blocks_of(s_seq[r], p.B) + (i - s_blk[r]);
     if (c < p.max_blocks) p.table[(size_t)r * p.max_blocks + c] = i < n_free ? p.free_blocks[n_free - 1 - i] : -1;
   }
   // Four rows a thread: B is a multiple of 16, so a thread whose rows belong to
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
   for (long long t0 = 4LL * first; t0 < p.n_rows; t0 += 4LL * step) {
     int slot[4], pos[4];
     int r = t0 < total ? last_not_above(s_row, p.R, (int)t0) : 0;
-    long long c_known = -1;
+    int c_known = -1;
     int blk = -1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -136,23 +139,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
           c_known = -1;
         }
         const int seq = s_seq[r];
-        const long long at = (long long)seq + (t - s_row[r]);
-        const long long c = at / p.B;
-        if (c != c_known) {
-          c_known = c;
+        const uint32_t at = (uint32_t)seq + (uint32_t)(t - s_row[r]);
+        const uint32_t c = at / (uint32_t)p.B;
+        if ((int)c != c_known) {
+          c_known = (int)c;
           blk = -1;
-          const long long have = ((long long)seq + p.B - 1) / p.B;
-          if (c < p.max_blocks) {
+          const uint32_t have = blocks_of(seq, p.B);
+          if (c < (uint32_t)p.max_blocks) {
             if (c < have) {
               blk = p.table[(size_t)r * p.max_blocks + c];
             } else {
-              const long long k = s_blk[r] + (c - have);
+              const long long k = s_blk[r] + (long long)(c - have);
               if (k < n_free) blk = p.free_blocks[n_free - 1 - k];
             }
           }
         }
         pos[i] = clamp_i32(at);
-        if (blk >= 0) slot[i] = clamp_i32((long long)blk * p.B + at % p.B);
+        if (blk >= 0) slot[i] = clamp_i32((long long)blk * p.B + (at - c * p.B));
       }
     }
     if (p.vec && t0 + 3 < p.n_rows) {
@@ -214,24 +217,27 @@ BWS_DEV void norm_head(float (&x)[8], const float (&w)[8], float eps) {
 }
 
 // cos and sin of position * inv_freq[i] for a row's rot / 2 pairs, in turns:
-// f = inv_freq / 2 pi, and only the turn's fraction is kept. Below 2^24 the
-// position is exact in FP32 and f two FP32 parts (48 bits, formed once per
-// warp): the high product is exact as a rounded product and its FMA remainder,
-// so whole turns leave it before the parts are added, without FP64 (which runs
-// at about 2 a clock and SM here). From 2^24 on the product is taken in FP64.
-// Either way the fraction is off by a few 2^-24.
+// f = inv_freq / 2 pi as two FP32 parts (48 bits, formed once per warp), and
+// only the turn's fraction is kept. Below 2^24 the position is exact in FP32:
+// the high product is exact as a rounded product and its FMA remainder, so
+// whole turns leave it before the parts are added. FP64 runs at about 2 a clock
+// and SM here (formed that way, f alone held the FP64 pipe 73 % busy in a
+// verify batch); only positions from 2^24 on take their product in it. Either
+// way the fraction is off by a few 2^-24.
 template <int D>
 struct Angles {
   static constexpr int kEach = D / 2 / Head<D>::kLanes;   // pairs a lane forms: sl + k * kLanes
   float fh[kEach], fl[kEach];
 
   BWS_DEV void init(const float* inv_freq, int half, int sl) {
+    constexpr double kTurn = 0.15915494309189533577;      // 1 / 2 pi
+    constexpr float kHi = (float)kTurn, kLo = (float)(kTurn - (double)kHi);
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
       const int i = sl + k * Head<D>::kLanes;
-      const double f = i < half ? (double)inv_freq[i] * 0.15915494309189533577 : 0.0;
-      fh[k] = (float)f;
-      fl[k] = (float)(f - (double)fh[k]);
+      const float f = i < half ? inv_freq[i] : 0.0f;
+      fh[k] = f * kHi;
+      fl[k] = fmaf(f, kLo, fmaf(f, kHi, -fh[k]));
     }
   }
   BWS_DEV void form(int pos, const float* inv_freq, int half, int sl, float2* cs) const {
@@ -414,15 +420,27 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 
   int t = t0;
   while (t < t1) {
-    // rows t - 1 .. t + 30's slots, a lane each; the first round's rows beside them
+    // Rows t - 1 .. t + 30's slots, a lane each: the first run that starts
+    // among them (from t on, inside the span).
     const int at = t - 1 + lane;
-    const int window = at >= 0 && at < in.n_rows ? in.slots[at] : -2;
-    uint4 raw = row_at(t + mine);
+    int window = at >= 0 && at < in.n_rows ? in.slots[at] : -2;
+    uint4 raw = row_at(t + mine);   // in a step of few rows, the run's
     int pos = pos_at(t + mine);
-    const int before = __shfl_sync(0xffffffffu, window, 0), slot = __shfl_sync(0xffffffffu, window, 1);
-    if (slot < 0 || slot >= n_slots) { ++t; continue; }
+    const int before = __shfl_up_sync(0xffffffffu, window, 1);
+    const bool starts = lane > 0 && at < t1 && window >= 0 && window < n_slots &&
+                        (window % B == 0 || before != window - 1);
+    const unsigned first = __ballot_sync(0xffffffffu, starts);
+    if (first == 0u) { t += 31; continue; }
+    const int skip = __ffs(first) - 2;
+    if (skip > 0) {
+      t += skip;
+      const int i = t - 1 + lane;
+      window = i < in.n_rows ? in.slots[i] : -2;
+      raw = row_at(t + mine);
+      pos = pos_at(t + mine);
+    }
+    const int slot = __shfl_sync(0xffffffffu, window, 1);
     const int off = slot % B, room = B - off;
-    if (off != 0 && before == slot - 1) { ++t; continue; }   // inside an earlier run
     // the run's rows: slots go on by one, inside the block
     const unsigned on = __ballot_sync(0xffffffffu, lane == 0 || (lane - 1 < room && window == slot + lane - 1));
     int m = on == 0xffffffffu ? 31 : __ffs(~on) - 2;
