@@ -46,6 +46,7 @@ constexpr int kUnit = 16;                  // cached tokens of a unit
 constexpr int kAttnMaxRows = kMaxTokens;   // rows of a request
 constexpr int kAttnMaxGroup = 16;          // query heads of a kv head
 constexpr uint32_t kAttnPolls = 1u << 22;
+constexpr float kNone = -3.0e38f;           // a running maximum of nothing
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -284,23 +285,28 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     return false;
   };
 
-  // ---- copies: 32 of the warp's units (first + warp, + 8, ...) at a time, a block id a lane
-  int mine, ids;
+  // ---- copies: 32 of the warp's units (first + warp, + 8, ...) at a time, a unit
+  // a lane: the block (-1: not there) and the token in it.
+  int mine, ids, toks;
   auto token_of = [&](int i) { return (sg.first + warp + i * kAttnWarps) * kUnit; };
-  auto block_of = [&](int i) {
-    int b = -1;
-    if (i < mine && token_of(i) < sg.rq.kv) b = p.table[(size_t)sg.r * p.max_blocks + token_of(i) / p.B];
-    return b >= 0 && b < p.n_blocks ? b : -1;
+  auto look_up = [&](int i, int& block, int& tok) {
+    block = -1;
+    tok = 0;
+    const int t = token_of(i);
+    if (i < mine && t < sg.rq.kv) {
+      const int q = t / p.B;
+      const int b = p.table[(size_t)sg.r * p.max_blocks + q];
+      tok = t - q * p.B;
+      block = b >= 0 && b < p.n_blocks ? b : -1;
+    }
   };
-  auto issue = [&](int i) {   // the whole warp; unit i of this warp into its stage
-    if ((i & 31) == 0 && i > 0) ids = block_of(i + lane);
-    const int b = __shfl_sync(0xffffffffu, ids, i & 31);
-    const int s = (int)((phase_base + i) % S::kStages);
+  auto issue = [&](int i, int s) {   // the whole warp; unit i of this warp into stage s
+    if ((i & 31) == 0 && i > 0) look_up(i + lane, ids, toks);
+    const int b = __shfl_sync(0xffffffffu, ids, i & 31), tok = __shfl_sync(0xffffffffu, toks, i & 31);
     if (lane == 0) {
       const uint32_t bar = bar0 + 8 * s, dst = ring + s * S::kStage;
       if (b >= 0) {
         mbar_arrive_expect_tx(bar, S::kStage);
-        const int tok = token_of(i) % p.B;
 #pragma unroll
         for (int x = 0; x < S::kPanels; ++x) {
           tma_load_4d(dst + x * kUnit * 128, &p.k, x * 128, tok, sg.head, b, bar, pol);
@@ -310,21 +316,29 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
         mbar_arrive(bar);
       }
     }
-    __syncwarp();
   };
-  // scales of 32 units, one a lane; ks = -1: the block is not there
-  float2 sc_l = make_float2(-1.0f, 0.0f), sc_n = sc_l;
+  // Scales of 32 units, one a lane: ks (-1: the block is not there), log2(vs), 1 / vs.
+  struct Scales {
+    float ks, lvs, rvs;
+  };
+  Scales sc_l, sc_n;
   auto scales_of = [&](int b) {
-    if (b < 0) return make_float2(-1.0f, 0.0f);
-    const size_t at = (size_t)b * p.K + sg.head;
-    return make_float2(p.k_scale[at], p.v_scale[at]);
+    Scales s = {-1.0f, 0.0f, 0.0f};
+    if (b >= 0) {
+      const size_t at = (size_t)b * p.K + sg.head;
+      s.ks = p.k_scale[at];
+      const float vs = fminf(fmaxf(p.v_scale[at], 0x1p-60f), 0x1p60f);
+      s.lvs = log2f(vs);
+      s.rvs = 1.0f / vs;
+    }
+    return s;
   };
   // A segment's start: its first copies, scales and this warp's query rows are
   // asked for together; nothing here waits but the copies for the block ids.
   uint16_t qx[NT][D / 32];
   auto open_segment = [&]() {
     mine = (sg.last - sg.first - warp + kAttnWarps - 1) / kAttnWarps;
-    ids = block_of(lane);
+    look_up(lane, ids, toks);
     const int n_rows = min(sg.rq.rows * p.G - sg.row0, S::kRows);
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
@@ -341,7 +355,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     }
     if (!dead) {
       const int ahead = min(mine, S::kStages);
-      for (int i = 0; i < ahead; ++i) issue(i);
+      for (int i = 0; i < ahead; ++i) issue(i, (int)((phase_base + i) % S::kStages));
     }
     sc_l = scales_of(ids);
   };
@@ -402,7 +416,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         qs[n][k] = T.q_scale[n * 8 + t4 * 2 + k];
-        m[n][k] = -INFINITY;
+        m[n][k] = kNone;
         l[n][k] = 0.0f;
       }
 #pragma unroll
@@ -426,19 +440,26 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
         }
         break;
       }
-      if ((i & 31) == 16) sc_n = scales_of(block_of((i & ~31) + 32 + lane));   // half a batch ahead
+      if ((i & 31) == 16) {   // half a batch ahead
+        int b, tok;
+        look_up((i & ~31) + 32 + lane, b, tok);
+        sc_n = scales_of(b);
+      }
       if ((i & 31) == 0 && i > 0) sc_l = sc_n;
-      const float2 sc = make_float2(__shfl_sync(0xffffffffu, sc_l.x, i & 31), __shfl_sync(0xffffffffu, sc_l.y, i & 31));
+      const float ks = __shfl_sync(0xffffffffu, sc_l.ks, i & 31);
       const int tok0 = token_of(i);
-      if (sc.x != -1.0f) {
-        const float vs = fminf(fmaxf(sc.y, 0x1p-60f), 0x1p60f);
-        const float lvs = log2f(vs), rvs = 1.0f / vs;
+      if (ks != -1.0f) {
+        const float lvs = __shfl_sync(0xffffffffu, sc_l.lvs, i & 31), rvs = __shfl_sync(0xffffffffu, sc_l.rvs, i & 31);
         // ---- S^T: 16 tokens x rows
-        float acc[NT][4];
+        // (two chains of sums, of even and of odd chunks, where the rows are few)
+        constexpr int kChains = NT == 1 ? 2 : 1;
+        float acc[kChains][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int j = 0; j < kChains; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[n][k] = 0.0f;
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[j][n][k] = 0.0f;
 #pragma unroll
         for (int c = 0; c < kMT; c += 2) {
           uint32_t w[4];
@@ -459,23 +480,27 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
                 b0 = b.x;
                 b1 = b.y;
               }
-              mma_f16_16816(acc[n], a0, a1, a2, a3, b0, b1);
+              mma_f16_16816(acc[h % kChains][n], a0, a1, a2, a3, b0, b1);
             }
           }
         }
         // ---- exponents, masks
+        float x[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[n][k] = fmaf(acc[n][k], sc.x * qs[n][k & 1], lvs);
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (kChains == 2) acc[0][n][k] += acc[1][n][k];
+            x[n][k] = fmaf(acc[0][n][k], ks * qs[n][k & 1], lvs);
+          }
         if (tok0 + kUnit - 1 > seen0) {   // the end: some rows do not see all 16
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int lim = min(seen0 + (row0 + n * 8 + t4 * 2 + k) / p.G, rq.kv - 1);
-              if (tok0 + g > lim) acc[n][k] = -INFINITY;
-              if (tok0 + g + 8 > lim) acc[n][k + 2] = -INFINITY;
+              if (tok0 + g > lim) x[n][k] = -INFINITY;
+              if (tok0 + g + 8 > lim) x[n][k + 2] = -INFINITY;
             }
           // Values no row or not every row may see: rows past the end are
           // zeroed (their memory may hold anything), and a NaN among the rows'
@@ -486,43 +511,41 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
             const int tk = b / (D / 4), byte = (b % (D / 4)) * 4, own = tok0 + tk - seen0;
             if (own <= 0) continue;
             const uint32_t at = vs_at + chunk_at<D>(tk, byte >> 4) + (byte & 15);
-            uint32_t x;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at));
+            uint32_t word;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(word) : "r"(at) : "memory");
             if (tok0 + tk >= rq.kv) {
-              x = 0;
+              word = 0;
             } else {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (((x >> (8 * k)) & 0x7Fu) == 0x7Fu) {
-                  x &= ~(0xFFu << (8 * k));
+                if (((word >> (8 * k)) & 0x7Fu) == 0x7Fu) {
+                  word &= ~(0xFFu << (8 * k));
                   atomicOr(&nan_mask[byte + k], 1u << own);
                 }
             }
-            asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(x) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(word) : "memory");
           }
           proxy_fence();   // before TMA writes the stage again
           __syncwarp();
         }
-        // ---- running maximum
-        float mn[NT][2];
+        // ---- running maximum: m follows only where an exponent passes it by
+        // more than 8, so that most units compare and vote and no more (weights
+        // up to 2^8 cost f16 and FP32 nothing)
         bool grew = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float v = fmaxf(acc[n][k], acc[n][k + 2]);
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
-            mn[n][k] = fmaxf(m[n][k], v);
-            grew |= mn[n][k] > m[n][k];
-          }
+          for (int k = 0; k < 4; ++k) grew |= x[n][k] > m[n][k & 1] + 8.0f;
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float f = mn[n][k] == -INFINITY ? 1.0f : exp2_fast(m[n][k] - mn[n][k]);
-              m[n][k] = mn[n][k];
+              float v = fmaxf(x[n][k], x[n][k + 2]);
+#pragma unroll
+              for (int y = 4; y < 32; y <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, y));
+              const float to = fmaxf(m[n][k], v), f = exp2_fast(m[n][k] - to);
+              m[n][k] = to;
               l[n][k] *= f;
 #pragma unroll
               for (int c = 0; c < kMT; ++c) {
@@ -537,10 +560,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
         for (int n = 0; n < NT; ++n) {
           float wv[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float mm = m[n][k & 1];
-            wv[k] = exp2_fast(acc[n][k] - (mm == -INFINITY ? 0.0f : mm));
-          }
+          for (int k = 0; k < 4; ++k) wv[k] = exp2_fast(x[n][k] - m[n][k & 1]);
           l[n][0] = fmaf(wv[0] + wv[2], rvs, l[n][0]);
           l[n][1] = fmaf(wv[1] + wv[3], rvs, l[n][1]);
           const __half2 h0 = __floats2half2_rn(wv[0], wv[1]), h1 = __floats2half2_rn(wv[2], wv[3]);
@@ -563,7 +583,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
         }
       }
       __syncwarp();
-      if (i + S::kStages < mine) issue(i + S::kStages);
+      if (i + S::kStages < mine) issue(i + S::kStages, s);
     }
     phase_base += mine;
     const int had = mine;
@@ -600,14 +620,13 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     if (S::kOverlap && more) store_queries(turn ^ 1);
     for (int e = tid; e < n_group_rows * (D / 4); e += kAttnThreads) {
       const int n = e / (D / 4), d = (e % (D / 4)) * 4;
-      float top = -INFINITY;
+      float top = kNone;
       for (int w = 0; w < n_live; ++w) top = fmaxf(top, T.m[w][n]);
       float sum = 0.0f;
       float4 a = make_float4(0, 0, 0, 0);
       for (int w = 0; w < n_live; ++w) {
         const float mw = T.m[w][n];
-        // a warp whose every weight is NaN still has m = -inf and must show
-        const float f = mw == top ? 1.0f : exp2_fast(mw - top);
+        const float f = exp2_fast(mw - top);
         const float4 b = *reinterpret_cast<const float4*>(join + w * kJoinStep + n * D + d);
         sum = fmaf(T.l[w][n], f, sum);
         a.x = fmaf(b.x, f, a.x);
@@ -683,7 +702,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   if (n >= min(rq.rows * p.G - row0, kRows)) return;
   auto slot_of = [&](int i) { return (c + i) * 2 + (i == 0 ? 1 : 0); };
   const int d4 = threadIdx.x % kLanes, at = threadIdx.x / kLanes;
-  float top = -INFINITY;
+  float top = kNone;
   for (int i = 0; i < pieces; ++i) top = fmaxf(top, p.part_ml[(size_t)slot_of(i) * kRows + n].x);
   float4 a = make_float4(0, 0, 0, 0);
   float l = 0.0f;
@@ -692,7 +711,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
     const size_t row = (size_t)slot_of(i) * kRows + n;
     const float2 ml = p.part_ml[row];
     const float4 b = reinterpret_cast<const float4*>(p.part_o + row * D)[d4];
-    const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
+    const float f = exp2_fast(ml.x - top);
     l = fmaf(ml.y, f, l);
     a.x = fmaf(b.x, f, a.x);
     a.y = fmaf(b.y, f, a.y);
@@ -878,7 +897,7 @@ int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_str
   p.part_o = reinterpret_cast<float*>(w + L.off_o);
   p.n_ctas = L.n_ctas;
   p.least = kAttnWarps;   // a unit for every warp
-  p.lead = 2048 / D;
+  p.lead = 32;
   cudaStream_t st = as_stream(stream);
   cudaError_t e;
   if (D == 64) e = launch_attn_d<64>(L.nt, p, st);

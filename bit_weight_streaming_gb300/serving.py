@@ -117,16 +117,18 @@ def kv_plan(seq_lens, new_lens, block_tokens, block_table, free_blocks, n_free, 
     _check("n_free", n_free, _I32, (1,))
     if n_rows < 0:
         raise BwsError("n_rows must not be negative")
-    # one allocation; each part starts on a 16-byte boundary
-    a, b = (n_rows + 3) & ~3, (R + 4) & ~3
-    buf = torch.empty(2 * a + 2 * b + 8, dtype=_I32, device=seq_lens.device)
-    at = buf.data_ptr()
+    # a tensor each: views of one cost more than the allocator
+    dev = seq_lens.device
+    slots = torch.empty(n_rows, dtype=_I32, device=dev)
+    positions = torch.empty_like(slots)
+    row_start = torch.empty(R + 1, dtype=_I32, device=dev)
+    kv_lens = torch.empty_like(seq_lens)
+    n_out = torch.empty_like(n_free)
+    status = torch.empty_like(n_free)
     _fail(lib().bws_kv_plan(seq_lens.data_ptr(), new_lens.data_ptr(), R, block_tokens, block_table.data_ptr(), wide,
-                            free_blocks.data_ptr(), n_free.data_ptr(), n_rows, at, at + 4 * a, at + 8 * a,
-                            at + 8 * a + 4 * b, at + 8 * (a + b), at + 8 * (a + b) + 16,
+                            free_blocks.data_ptr(), n_free.data_ptr(), n_rows, slots.data_ptr(), positions.data_ptr(),
+                            row_start.data_ptr(), kv_lens.data_ptr(), n_out.data_ptr(), status.data_ptr(),
                             _raw_stream(seq_lens.get_device())), "bws_kv_plan")
-    slots, _, positions, _, row_start, _, kv_lens, _, n_out, _, status, _ = buf.split(
-        (n_rows, a - n_rows, n_rows, a - n_rows, R + 1, b - R - 1, R, b - R, 1, 3, 1, 3))
     return KvPlan(slots, positions, row_start, kv_lens, n_out, status)
 
 
@@ -232,11 +234,10 @@ def draft_verify(target, tokens, row_start, accept_u, sample_u, max_rows, draft=
     _check("row_start", row_start, _I32, (R + 1,))
     if max_rows < 1:
         raise BwsError("max_rows must be positive")
-    buf = torch.empty((R * (max_rows + 1),), dtype=_I32, device=target.device)
-    out, n_out = buf.split((R * max_rows, R))
-    at = buf.data_ptr()
+    out = torch.empty((R, max_rows), dtype=_I32, device=target.device)
+    n_out = torch.empty_like(sample_u, dtype=_I32)
     _fail(lib().bws_draft_verify(target.data_ptr(), strides[0], None if draft is None else draft.data_ptr(), strides[1],
                                  tokens.data_ptr(), T, V, row_start.data_ptr(), R, accept_u.data_ptr(),
-                                 sample_u.data_ptr(), max_rows, at, at + 4 * R * max_rows,
+                                 sample_u.data_ptr(), max_rows, out.data_ptr(), n_out.data_ptr(),
                                  _raw_stream(target.get_device())), "bws_draft_verify")
-    return out.view(R, max_rows), n_out
+    return out, n_out
