@@ -174,17 +174,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
 
 // ---- norm, rotation, cache write ------------------------------------------------
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
 
 struct AppendParams {
   bws_qkv in;
   bws_kv_cache c;
   uint16_t* q_out;
-  int span;          // rows whose runs one key/value CTA writes
+  int span;          // rows whose runs one key/value CTA writes, or one warp of it:
+  int own_spans;
   int n_kv_ctas;     // spans * kv heads * 2, before the query CTAs
   int heads_per;     // query heads a warp takes of one row
-  int stage_rows;    // rows of a run kept in shared memory between the two passes
+  int solo_rows;     // the longest run that one warp takes
+  int stage_rows;    // rows of a longer run kept in shared memory between the passes
 };
 
 // A head is held eight values a lane by D / 8 neighbouring lanes ("group"), so
@@ -224,6 +226,12 @@ BWS_DEV void norm_head(float (&x)[8], const float (&w)[8], float eps) {
 // and SM here (formed that way, f alone held the FP64 pipe 73 % busy in a
 // verify batch); only positions from 2^24 on take their product in it. Either
 // way the fraction is off by a few 2^-24.
+// The turn of a far position: FP64, out of line so that nothing of it runs for near ones.
+__device__ __noinline__ float far_turn(float f, int pos) {
+  const double d = (double)f * 0.15915494309189533577 * (double)pos;
+  return (float)(d - rint(d));
+}
+
 template <int D>
 struct Angles {
   static constexpr int kEach = D / 2 / Head<D>::kLanes;   // pairs a lane forms: sl + k * kLanes
@@ -253,11 +261,13 @@ struct Angles {
         t = (a - rintf(a)) + fmaf(fl[k], fp, e);
         t -= rintf(t);
       } else {
-        const double d = (double)inv_freq[i] * 0.15915494309189533577 * (double)pos;
-        t = (float)(d - rint(d));
+        t = far_turn(inv_freq[i], pos);
       }
+      // Within half a turn the fast pair is off by at most 2^-21, far below
+      // the 2^-9 and 2^-4 that the results are rounded by; sincospif's forty
+      // instructions a pair were a third of a key row's work.
       float s, c;
-      sincospif(2.0f * t, &s, &c);
+      __sincosf(t * 6.2831853071795865f, &s, &c);
       cs[i] = make_float2(c, s);
     }
   }
@@ -324,20 +334,19 @@ BWS_DEV void store_codes(uint8_t* p, const float (&x)[8], float inv) {
 
 // Query warps take Head::kRows rows and heads_per heads of them, whose angles
 // they form once. Key/value CTAs: one span of rows, one kv head, one side; each
-// run of rows that starts in the span is normed and rotated by the warps, its
-// largest magnitude joined over the CTA, and written under the scale that
-// follows. Between the two passes the values wait in shared memory (the first
-// stage_rows rows; the rest, in long runs of wide heads, are formed again: the
-// rows are in L1 by then). Every loop asks for its next rows before it works on
-// the ones it has.
+// run of rows that starts in the span is normed and rotated, its largest
+// magnitude found, and written under the scale that follows. Between the two
+// passes the values wait in shared memory (of a run that is longer than it, the
+// rest is formed again: the rows are in L1 by then). One rolled loop serves
+// short and long runs: with the short ones unrolled in registers a quarter of
+// the issue slots waited for instructions (a 12382-row chunk: 128 us).
 // Bound: launch and three dependent loads for a decoded token, the bytes of
 // the rows for a prompt chunk.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_constant__ AppendParams p) {
   using Hd = Head<D>;
   constexpr int kStep = kAppendWarps * Hd::kRows;   // rows of a key/value CTA's round
   extern __shared__ __align__(16) float s_stage[];  // [stage_rows][D]
-  __shared__ __align__(16) float s_buf[kAppendWarps][Hd::kRows][D];
   __shared__ __align__(16) float2 s_cs[kAppendWarps][Hd::kRows][D / 2];
   __shared__ float s_amax[kAppendWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -345,7 +354,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   const bws_qkv& in = p.in;
   const int half = in.rot >> 1;
   float2* const cs = s_cs[warp][sub];
-  float* const buf = s_buf[warp][sub];
+  float* const buf = s_stage + p.stage_rows * D + (warp * Hd::kRows + sub) * D;   // there where a pair needs it
   pdl_launch_dependents();
   pdl_wait();
   Angles<D> angles;
@@ -393,12 +402,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   const bws_kv_cache& c = p.c;
   const int B = c.block_tokens, K = c.n_kv_heads;
   const int side = blockIdx.x & 1, head = (int)(blockIdx.x >> 1) % K;
-  const int t0 = (int)((blockIdx.x >> 1) / K) * p.span, t1 = min(t0 + p.span, in.n_rows);
+  const int group = (int)((blockIdx.x >> 1) / K);
+  const int t0 = (p.own_spans ? group * kAppendWarps + warp : group) * p.span, t1 = min(t0 + p.span, in.n_rows);
   const long long n_slots = (long long)c.n_blocks * B;
   const long long row_stride = side ? in.v_row_stride : in.k_row_stride;
   const uint16_t* src = (side ? in.v + head * in.v_head_stride : in.k + head * in.k_head_stride) + sl * 8;
   const bool normed = !side && in.k_weight != nullptr, turned = !side && half > 0;
-  const int mine = warp * Hd::kRows + sub;   // this group's first row of a round
   auto row_at = [&](int row) { return *reinterpret_cast<const uint4*>(src + min(row, in.n_rows - 1) * row_stride); };
   auto pos_at = [&](int row) { return turned ? in.positions[min(row, in.n_rows - 1)] : 0; };
   float w[8];
@@ -418,107 +427,123 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     }
   };
 
-  int t = t0;
-  while (t < t1) {
-    // Rows t - 1 .. t + 30's slots, a lane each: the first run that starts
-    // among them (from t on, inside the span).
+  // The runs that start in the span, in order. Where the CTA shares it, every
+  // warp finds them all; a short one is a warp's alone, with no barrier; a long
+  // one is the whole CTA's.
+  auto largest = [&](const float (&x)[8], float amax) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float a = fabsf(x[k]);
+      if (a < INFINITY) amax = fmaxf(amax, a);   // NaN and infinity set no scale
+    }
+    return amax;
+  };
+
+  int turn = 0;   // short runs so far
+  for (int t = t0; t < t1; t += 31) {
+    // rows t - 1 .. t + 30's slots, a lane each
     const int at = t - 1 + lane;
-    int window = at >= 0 && at < in.n_rows ? in.slots[at] : -2;
-    uint4 raw = row_at(t + mine);   // in a step of few rows, the run's
-    int pos = pos_at(t + mine);
+    const int window = at >= 0 && at < in.n_rows ? in.slots[at] : -2;
     const int before = __shfl_up_sync(0xffffffffu, window, 1);
-    const bool starts = lane > 0 && at < t1 && window >= 0 && window < n_slots &&
-                        (window % B == 0 || before != window - 1);
-    const unsigned first = __ballot_sync(0xffffffffu, starts);
-    if (first == 0u) { t += 31; continue; }
-    const int skip = __ffs(first) - 2;
-    if (skip > 0) {
-      t += skip;
-      const int i = t - 1 + lane;
-      window = i < in.n_rows ? in.slots[i] : -2;
-      raw = row_at(t + mine);
-      pos = pos_at(t + mine);
-    }
-    const int slot = __shfl_sync(0xffffffffu, window, 1);
-    const int off = slot % B, room = B - off;
-    // the run's rows: slots go on by one, inside the block
-    const unsigned on = __ballot_sync(0xffffffffu, lane == 0 || (lane - 1 < room && window == slot + lane - 1));
-    int m = on == 0xffffffffu ? 31 : __ffs(~on) - 2;
-    if (m == 31) {
-      while (m < room) {
-        const int i = m + lane;
-        const bool more = i < room && t + i < in.n_rows && in.slots[t + i] == slot + i;
-        const unsigned b = __ballot_sync(0xffffffffu, more);
-        const int n = b == 0xffffffffu ? 32 : __ffs(~b) - 1;
-        m += n;
-        if (n < 32) break;
-      }
-    }
-    const int block = slot / B;
-    float* scale_at = (side ? c.v_scale : c.k_scale) + (size_t)block * K + head;
-    const float old = *scale_at;
-    float amax = 0.0f;
-    for (int i0 = 0; i0 < m; i0 += kStep) {
-      const int i = i0 + mine;
-      const uint4 now = raw;
-      const int here = pos;
-      if (i0 + kStep < m) {
-        raw = row_at(t + i + kStep);
-        pos = pos_at(t + i + kStep);
-      }
-      float x[8];
-      form(now, here, x);
-      if (i < m) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float a = fabsf(x[k]);
-          if (a < INFINITY) amax = fmaxf(amax, a);   // NaN and infinity set no scale
-        }
-        if (i < p.stage_rows) {
-          float4* st = reinterpret_cast<float4*>(s_stage + i * D + sl * 8);
-          st[0] = make_float4(x[0], x[1], x[2], x[3]);
-          st[1] = make_float4(x[4], x[5], x[6], x[7]);
+    const bool live = window >= 0 && window < n_slots;
+    const bool fresh = !live || window % B == 0 || before != window - 1;   // not the next row of a run
+    const unsigned breaks = __ballot_sync(0xffffffffu, fresh);
+    unsigned starts = __ballot_sync(0xffffffffu, fresh && live && lane > 0 && at < t1);
+    while (starts != 0u) {
+      const int j = __ffs(starts) - 1;
+      starts &= starts - 1;
+      const int row = t - 1 + j;   // the run's first
+      const int slot = __shfl_sync(0xffffffffu, window, j);
+      const int off = slot % B, room = B - off, block = slot / B;
+      const unsigned next = j < 31 ? breaks >> (j + 1) : 0u;
+      int m = next != 0u ? __ffs(next) : 32 - j;
+      if (next == 0u) {   // past the window
+        while (m < room) {
+          const int i = m + lane;
+          const bool on = i < room && row + i < in.n_rows && in.slots[row + i] == slot + i;
+          const unsigned b = __ballot_sync(0xffffffffu, on);
+          const int n = b == 0xffffffffu ? 32 : __ffs(~b) - 1;
+          m += n;
+          if (n < 32) break;
         }
       }
-    }
-    amax = warp_max(amax);
-    if (lane == 0) s_amax[warp] = amax;
-    __syncthreads();
+      float* scale_at = (side ? c.v_scale : c.k_scale) + (size_t)block * K + head;
+      const bool solo = p.own_spans || m <= p.solo_rows;
+      if (solo && !p.own_spans && turn++ % kAppendWarps != warp) continue;
+      const int step = solo ? Hd::kRows : kStep, mine = (solo ? 0 : warp * Hd::kRows) + sub;
+      float* const stage = s_stage + (solo ? warp * p.solo_rows * D : 0) + sl * 8;
+      const int staged = solo ? p.solo_rows : p.stage_rows;
+      const float old = *scale_at;
+      float amax = 0.0f;
+      uint4 raw = row_at(row + mine);
+      int pos = pos_at(row + mine);
+#pragma unroll 1
+      for (int i0 = 0; i0 < m; i0 += step) {
+        const int i = i0 + mine;
+        const uint4 now = raw;
+        const int here = pos;
+        if (i0 + step < m) {
+          raw = row_at(row + i + step);
+          pos = pos_at(row + i + step);
+        }
+        float x[8];
+        form(now, here, x);
+        if (i < m) {
+          float top = 0.0f;   // NaN and infinity set no scale
 #pragma unroll
-    for (int i = 0; i < kAppendWarps; ++i) amax = fmaxf(amax, s_amax[i]);
-    const float need = exp2i(scale_exponent(amax));
-    const float scale = off == 0 ? need : fmaxf(old, need);
-    const float inv = 1.0f / scale;
-    uint8_t* codes = (side ? c.v : c.k) + (size_t)block * c.block_stride + (size_t)head * c.head_stride;
-    if (off != 0 && scale != old) {   // the scale grew: the block's earlier codes again, under it
-      const float f = old / scale;
-      uint32_t* w32 = reinterpret_cast<uint32_t*>(codes);
-      for (int i = threadIdx.x; i < off * (D / 4); i += kAppendThreads) {
-        uint32_t lo, hi;
-        e4m3x4_to_f16x2x2(w32[i], lo, hi);
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        w32[i] = f32x2_to_e4m3x2(a.y * f, a.x * f) | (f32x2_to_e4m3x2(b.y * f, b.x * f) << 16);
+          for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
+          if (top == INFINITY) {
+            top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = fabsf(x[k]) < INFINITY ? fmaxf(top, fabsf(x[k])) : top;
+          }
+          amax = fmaxf(amax, top);
+          if (i < staged) {
+            float4* st = reinterpret_cast<float4*>(stage + i * D);
+            st[0] = make_float4(x[0], x[1], x[2], x[3]);
+            st[1] = make_float4(x[4], x[5], x[6], x[7]);
+          }
+        }
       }
-    }
-    uint8_t* dst = codes + (size_t)off * D + sl * 8;
-    for (int i0 = 0; i0 < m; i0 += kStep) {
-      const int i = i0 + mine;
-      float x[8];
-      if (i0 + kStep <= p.stage_rows || m <= p.stage_rows) {   // the same for the whole warp
-        if (i >= m) continue;
-        const float4* st = reinterpret_cast<const float4*>(s_stage + i * D + sl * 8);
+      amax = warp_max(amax);
+      if (!solo) {
+        if (lane == 0) s_amax[warp] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kAppendWarps; ++i) amax = fmaxf(amax, s_amax[i]);
+      }
+      const float need = exp2i(scale_exponent(amax));
+      const float scale = off == 0 ? need : fmaxf(old, need), inv = 1.0f / scale;
+      uint8_t* codes = (side ? c.v : c.k) + (size_t)block * c.block_stride + (size_t)head * c.head_stride;
+      if (off != 0 && scale != old) {   // the scale grew: the block's earlier codes again, under it
+        const float f = old / scale;
+        uint32_t* w32 = reinterpret_cast<uint32_t*>(codes);
+        for (int i = solo ? lane : threadIdx.x; i < off * (D / 4); i += solo ? 32 : kAppendThreads) {
+          uint32_t lo, hi;
+          e4m3x4_to_f16x2x2(w32[i], lo, hi);
+          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+          w32[i] = f32x2_to_e4m3x2(a.y * f, a.x * f) | (f32x2_to_e4m3x2(b.y * f, b.x * f) << 16);
+        }
+      }
+      uint8_t* dst = codes + (size_t)off * D + sl * 8;
+      const int kept = min(m, staged);
+      for (int i = mine; i < kept; i += step) {
+        const float4* st = reinterpret_cast<const float4*>(stage + i * D);
         const float4 a = st[0], b = st[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-      } else {
-        form(row_at(t + i), pos_at(t + i), x);
+        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        store_codes(dst + (size_t)i * D, x, inv);
       }
-      if (i < m) store_codes(dst + (size_t)i * D, x, inv);
+#pragma unroll 1
+      for (int i0 = staged; i0 < m; i0 += step) {   // staged is a multiple of step
+        const int i = i0 + mine;
+        float x[8];
+        form(row_at(row + i), pos_at(row + i), x);
+        if (i < m) store_codes(dst + (size_t)i * D, x, inv);
+      }
+      if (!solo) __syncthreads();   // every thread has read the old scale and s_amax
+      if (solo ? lane == 0 : threadIdx.x == 0) *scale_at = scale;
     }
-    __syncthreads();   // every thread has read the old scale and s_amax
-    if (threadIdx.x == 0) *scale_at = scale;
-    t += m;
   }
 }
 
@@ -535,6 +560,13 @@ cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem, cud
   cfg.attrs = a;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D>
+cudaError_t launch_append(unsigned grid, size_t smem, cudaStream_t st, const AppendParams& p) {
+  static std::atomic<unsigned long long> attr{0};
+  const cudaError_t e = set_smem_once(attr, append_kernel<D>, kAppendWarps * 9 * 256 * 4);
+  return e != cudaSuccess ? e : launch_pdl(append_kernel<D>, grid, kAppendThreads, smem, st, p);
 }
 
 }  // namespace
@@ -634,14 +666,16 @@ int bws_qk_norm_rope_append(const bws_qkv* in, const bws_kv_cache* cache, uint16
   p.c = *cache;
   p.q_out = q_out;
   const long long sms = num_sms();
-  // A span of one row gives every row of a decode batch its own CTA; longer
-  // calls take more, up to a block, so that few CTAs are launched only to find
-  // that their rows belong to an earlier run.
-  const long long rows = in->n_rows;
-  long long span = rows * K * 2 / (sms * 8);
-  span = span < 1 ? 1 : span > cache->block_tokens ? cache->block_tokens : span;
+  // Where the blocks alone are work for eight warps an SM, every warp takes a
+  // span of its own, a block long. Else a CTA's warps share one: eight rows at
+  // least, which in a decode batch are a run for each.
+  const long long rows = in->n_rows, B = cache->block_tokens;
+  p.own_spans = rows * K * 2 >= sms * 8 * B;
+  long long span = p.own_spans ? B : rows * K * 2 / (sms * 4);
+  span = span < kAppendWarps ? kAppendWarps : span > kAppendWarps * B ? kAppendWarps * B : span;
   p.span = (int)span;
-  const long long spans = (rows + span - 1) / span;
+  const long long per_cta = p.own_spans ? span * kAppendWarps : span;
+  const long long spans = (rows + per_cta - 1) / per_cta;
   const long long kv_ctas = spans * K * 2;
   // heads of a row that share a warp's angles, as long as every SM keeps 8 warps
   const long long row_groups = (rows + 256 / D - 1) / (256 / D);
@@ -652,17 +686,19 @@ int bws_qk_norm_rope_append(const bws_qkv* in, const bws_kv_cache* cache, uint16
   const long long q_ctas = (row_groups * groups + kAppendWarps - 1) / kAppendWarps;
   if (kv_ctas + q_ctas >= (1LL << 31)) return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: too many rows", name);
   p.n_kv_ctas = (int)kv_ctas;
-  long long stage = 32 * 1024 / (4 * D);
-  if (stage > cache->block_tokens) stage = cache->block_tokens;
-  if (stage > rows) stage = rows;
-  p.stage_rows = (int)stage;
-  const size_t smem = (size_t)stage * D * 4;
+  // A warp takes runs of up to eight rounds where the rows are many, two where
+  // a run's other warps would have nothing to do.
+  const int round = 256 / D;
+  p.solo_rows = round * (rows * K * 2 >= sms * 16 ? 8 : 2);
+  p.stage_rows = kAppendWarps * p.solo_rows;
+  const bool pair_buffer = !in->interleaved && (in->rot / 2) % 8 != 0;
+  const size_t smem = (size_t)p.stage_rows * D * 4 + (pair_buffer ? kAppendWarps * 256 * 4 : 0);
   const unsigned grid = (unsigned)(kv_ctas + q_ctas);
   cudaStream_t st = as_stream(stream);
   cudaError_t e;
-  if (D == 64) e = launch_pdl(append_kernel<64>, grid, kAppendThreads, smem, st, p);
-  else if (D == 128) e = launch_pdl(append_kernel<128>, grid, kAppendThreads, smem, st, p);
-  else e = launch_pdl(append_kernel<256>, grid, kAppendThreads, smem, st, p);
+  if (D == 64) e = launch_append<64>(grid, smem, st, p);
+  else if (D == 128) e = launch_append<128>(grid, smem, st, p);
+  else e = launch_append<256>(grid, smem, st, p);
   return cuda_status(e, name);
 }
 
