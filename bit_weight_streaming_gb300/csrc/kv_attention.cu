@@ -26,169 +26,20 @@
 // reads without bank conflicts) and keeps its own m, l and O in registers; no
 // barrier joins them before the segment's end.
 // Bound: HBM for few rows; the conversions and mma.sync for many.
-#include <cuda.h>
 #include <string.h>
 
 #include <atomic>
 
-#include "bws_abi_util.h"
-#include "bws_common.cuh"
-#include "bws_internal.h"
+#include "kv_attention.cuh"
 #include "kv_cache.cuh"
 #include "stream_tile.cuh"
 
 namespace bws {
 namespace {
 
-constexpr int kAttnWarps = 8;
-constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kUnit = 16;                  // cached tokens of a unit
-constexpr int kAttnMaxRows = kMaxTokens;   // rows of a request
-constexpr int kAttnMaxGroup = 16;          // query heads of a kv head
-constexpr uint32_t kAttnPolls = 1u << 22;
-constexpr float kNone = -3.0e38f;           // a running maximum of nothing
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct AttnParams {
-  CUtensorMap k, v;
-  const uint16_t* q;
-  long long q_row_stride, q_head_stride;
-  int n_rows, H, K, G;
-  int B, n_blocks;
-  const float *k_scale, *v_scale;
-  const int32_t* table;
-  int max_blocks, R;
-  const int32_t *row_start, *kv_lens;
-  int max_rows;
-  float scale;
-  uint16_t* out;
-  float* lse;
-  float* part_o;      // [2 * CTAs][8 NT][D]
-  float2* part_ml;    // [2 * CTAs][8 NT]
-  uint32_t* failed;   // [CTAs]
-  uint32_t* hdr;
-  int n_ctas, least;  // CTAs; smallest share in units
-  int lead;           // what a segment costs beside its units, in units
-};
-
-// ---- the line of units -----------------------------------------------------------
-
-struct Request {
-  int rows, start, kv, units, groups;   // kv: cached tokens; units of one segment; row groups
-};
-
-BWS_DEV Request request_of(const AttnParams& p, int r, int group_rows) {
-  Request q;
-  q.start = min(max(p.row_start[r], 0), p.n_rows);
-  q.rows = min(max(p.row_start[r + 1] - q.start, 0), min(p.max_rows, p.n_rows - q.start));
-  const long long cap = (long long)p.max_blocks * p.B;
-  q.kv = (int)min((long long)max(p.kv_lens[r], 0), cap);
-  q.units = max(1, (q.kv + kUnit - 1) / kUnit);   // a request without tokens still writes its rows
-  q.groups = (q.rows * p.G + group_rows - 1) / group_rows;
-  return q;
-}
-
-BWS_DEV long long length_of(const AttnParams& p, const Request& q) {
-  return (long long)p.K * q.groups * (p.lead + q.units);
-}
-
-// One CTA's part of a segment: units [first, last).
-struct Segment {
-  Request rq;
-  int r, head, row0, first, last;
-  bool whole;      // the CTA has every unit
-  bool starts;     // the CTA has the first unit
-};
-
-struct Line {
-  long long total, share;
-  int r;            // request that holds the asked position
-  long long base;   // its first position
-};
-
-// The whole CTA: the line's length, the share, and the request at position
-// pick(share), if the line has it.
-template <class Pick>
-BWS_DEV Line find_on_line(const AttnParams& p, int group_rows, Pick pick, long long* s_warp, long long* s_found) {
-  const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.R + n - 1) / n;
-  const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
-  long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += length_of(p, request_of(p, r, group_rows));
-  long long inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += a;
-  }
-  if (lane == 31) s_warp[warp] = inc;
-  __syncthreads();
-  long long before = inc - mine, total = 0;
-  for (int w = 0; w < n / 32; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
-  }
-  Line line;
-  line.total = total;
-  long long share = (total + p.n_ctas - 1) / p.n_ctas;
-  line.share = share < p.least ? p.least : share;
-  const long long u = pick(line.share);
-  if (u >= before && u < before + mine) {
-    long long b = before;
-    int r = r0;
-    for (; r < r1 - 1; ++r) {
-      const long long k = length_of(p, request_of(p, r, group_rows));
-      if (u < b + k) break;
-      b += k;
-    }
-    s_found[0] = r;
-    s_found[1] = b;
-  }
-  __syncthreads();
-  line.r = (int)s_found[0];
-  line.base = s_found[1];
-  return line;
-}
-
-// ---- tiles ---------------------------------------------------------------------
-
-BWS_DEV void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w, uint32_t bar, uint64_t pol) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;"
-      :: "r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(pol) : "memory");
-}
-BWS_DEV void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-BWS_DEV void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-BWS_DEV uint32_t transpose_8x8(uint32_t x) {
-  uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-BWS_DEV uint2 lds_v2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
-BWS_DEV float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-BWS_DEV void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
 template <int D, int NT>
 struct Shape {
-  static constexpr int kRowBytes = D < 128 ? D : 128;         // bytes of a swizzled row
-  static constexpr int kPanels = D / kRowBytes;               // panels of 16 tokens x kRowBytes
-  static constexpr int kSide = kUnit * D;                     // bytes of a unit's keys, or values
+  static constexpr int kSide = kBox * D;                     // bytes of a unit's keys, or values
   static constexpr int kStage = 2 * kSide;
   static constexpr int kRows = 8 * NT;
   static constexpr int kJoin = kRows * D * 4;                 // a warp's O in FP32, for the segment's end
@@ -217,13 +68,6 @@ struct __align__(16) Tail {
   uint32_t failed;
 };
 
-// Byte offset of 16-byte chunk `c` of token row `row` in a side.
-template <int D>
-BWS_DEV uint32_t chunk_at(int row, int c) {
-  if constexpr (D == 64) return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-  else return (c >> 3) * (kUnit * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel(const __grid_constant__ AttnParams p) {
   using S = Shape<D, NT>;
@@ -246,49 +90,18 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
   pdl_launch_dependents();
   pdl_wait();
   const int cta = blockIdx.x;
-  const Line line = find_on_line(p, S::kRows, [&](long long share) { return cta * share; }, T.line_warp, T.line_found);
-  const long long u0 = cta * line.share, u1 = min(line.total, u0 + line.share);
+  Walk walk(p, S::kRows, T.line_warp, T.line_found);
   const uint64_t pol = l2_evict_first();
   uint32_t phase_base = 0;   // units this warp has put through its ring
   bool dead = false;
   // this lane's ldmatrix row: tokens 0-7 and 8-15 of one chunk, then of the next
   const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lchunk = lane >> 4;
 
-  // ---- the CTA's segments, one after the other
-  long long u = u0, rbase = line.base;
-  int at_r = line.r;
-  Segment sg;
-  auto next_segment = [&]() {   // false: the share is done
-    while (u < u1) {
-      const Request rq = request_of(p, at_r, S::kRows);
-      const long long rn = length_of(p, rq);
-      if (u >= rbase + rn) {
-        rbase += rn;
-        ++at_r;
-        continue;
-      }
-      const int len = p.lead + rq.units, seg = (int)((u - rbase) / len);
-      const long long a = rbase + (long long)seg * len, b = a + len, first_unit = a + p.lead;
-      const long long from = max(u, first_unit), to = min(u1, b);
-      u = to;
-      if (from >= to) continue;   // the share ends before the first unit
-      sg.rq = rq;
-      sg.r = at_r;
-      sg.head = seg / rq.groups;
-      sg.row0 = (seg % rq.groups) * S::kRows;
-      sg.first = (int)(from - first_unit);
-      sg.last = (int)(to - first_unit);
-      sg.starts = first_unit >= u0;
-      sg.whole = sg.starts && to == b;
-      return true;
-    }
-    return false;
-  };
-
+  Segment sg = {};
   // ---- copies: 32 of the warp's units (first + warp, + 8, ...) at a time, a unit
   // a lane: the block (-1: not there) and the token in it.
   int mine, ids, toks;
-  auto token_of = [&](int i) { return (sg.first + warp + i * kAttnWarps) * kUnit; };
+  auto token_of = [&](int i) { return (sg.first + warp + i * kAttnWarps) * kBox; };
   auto look_up = [&](int i, int& block, int& tok) {
     block = -1;
     tok = 0;
@@ -307,11 +120,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
       const uint32_t bar = bar0 + 8 * s, dst = ring + s * S::kStage;
       if (b >= 0) {
         mbar_arrive_expect_tx(bar, S::kStage);
-#pragma unroll
-        for (int x = 0; x < S::kPanels; ++x) {
-          tma_load_4d(dst + x * kUnit * 128, &p.k, x * 128, tok, sg.head, b, bar, pol);
-          tma_load_4d(dst + S::kSide + x * kUnit * 128, &p.v, x * 128, tok, sg.head, b, bar, pol);
-        }
+        tma_load_box(dst, &p.k, tok, sg.head, b, bar, pol);
+        tma_load_box(dst + S::kSide, &p.v, tok, sg.head, b, bar, pol);
       } else {
         mbar_arrive(bar);
       }
@@ -382,7 +192,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     for (int i = tid; i < D; i += kAttnThreads) T.nan_mask[slot][i] = 0;
   };
 
-  bool more = next_segment();
+  bool more = walk.next(p, S::kRows, sg);
   int turn = 0;
   if (more) {
     open_segment();
@@ -493,7 +303,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
             if constexpr (kChains == 2) acc[0][n][k] += acc[1][n][k];
             x[n][k] = fmaf(acc[0][n][k], ks * qs[n][k & 1], lvs);
           }
-        if (tok0 + kUnit - 1 > seen0) {   // the end: some rows do not see all 16
+        if (tok0 + kBox - 1 > seen0) {   // the end: some rows do not see all 16
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -507,7 +317,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
           // own tokens is taken out here and put back at the end for the rows
           // that do see it; 0 * NaN would reach the others.
           __syncwarp();
-          for (int b = lane; b < kUnit * (D / 4); b += 32) {
+          for (int b = lane; b < kBox * (D / 4); b += 32) {
             const int tk = b / (D / 4), byte = (b % (D / 4)) * 4, own = tok0 + tk - seen0;
             if (own <= 0) continue;
             const uint32_t at = vs_at + chunk_at<D>(tk, byte >> 4) + (byte & 15);
@@ -590,7 +400,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     const int n_live = min(cur.last - cur.first, kAttnWarps);   // warps that had a unit
 
     // ---- the segment's end: join the warps' m, l, O
-    more = next_segment();
+    more = walk.next(p, S::kRows, sg);
     if (S::kOverlap && more) open_segment();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -666,12 +476,11 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
 
 // Joins the partial results of the segment that share x starts and does not
 // end; one row a CTA of the y axis, one float a thread.
-template <int D, int NT>
+template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kRows = 8 * NT;
+  const int kRows = p.group_rows;
   constexpr int kLanes = D / 4;            // threads of a row
   constexpr int kPer = 256 / kLanes;       // pieces read side by side
-  __shared__ long long s_warp[8], s_found[2];
   __shared__ float4 s_a[kPer][kLanes];
   __shared__ float s_l[kPer];
   __shared__ uint32_t s_bad;
@@ -689,17 +498,11 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
       p.hdr[1] = s_bad ? (uint32_t)BWS_STATUS_WAIT_TIMEOUT : 0u;
     }
   }
-  const Line line = find_on_line(p, kRows, [&](long long share) { return (c + 1) * share - 1; }, s_warp, s_found);
-  const long long u1 = (c + 1) * line.share;
-  if (u1 >= line.total) return;   // the last share: its segment ends in it
-  const Request rq = request_of(p, line.r, kRows);
-  const int len = p.lead + rq.units, seg = (int)((u1 - 1 - line.base) / len);
-  const long long seg_a = line.base + (long long)seg * len, seg_b = seg_a + len, first_unit = seg_a + p.lead;
-  if (first_unit < u1 - line.share || first_unit >= u1 || seg_b <= u1) return;   // starts elsewhere, or ends here
-  const int pieces = (int)((seg_b - 1) / line.share) - c + 1;
-  const int head = seg / rq.groups, row0 = (seg % rq.groups) * kRows;
+  const int4 cut = p.cut[2 * c];
+  const int pieces = p.cut[2 * c + 1].x;
   const int n = blockIdx.y;
-  if (n >= min(rq.rows * p.G - row0, kRows)) return;
+  if (pieces < 2 || n >= cut.y) return;
+  const int head = cut.z, row0 = cut.w;
   auto slot_of = [&](int i) { return (c + i) * 2 + (i == 0 ? 1 : 0); };
   const int d4 = threadIdx.x % kLanes, at = threadIdx.x / kLanes;
   float top = kNone;
@@ -732,7 +535,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
     l += s_l[i];
   }
   const int j = (row0 + n) / p.G, h = head * p.G + (row0 + n) % p.G;
-  const size_t o = (size_t)(rq.start + j) * p.H + h;
+  const size_t o = (size_t)(cut.x + j) * p.H + h;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
   reinterpret_cast<uint2*>(p.out + o * D)[d4] =
@@ -742,33 +545,44 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
 
 // ---- host ------------------------------------------------------------------------
 
-// n8 tiles of a row group: the rows of a full request, rounded up to a form
-// that is built; more rows than fit the registers (NT * D <= 512) go in several
-// groups, each of which reads the cache again.
-int tiles_for(int D, int rows) {
-  const int most = 512 / D, want = (rows + 7) / 8;
+// The kernel and its n8 tiles for a request's rows. A warp of attn_kernel holds
+// O for every dimension, NT * D <= 512; more rows of a wide head go to the other
+// kernel, up to 64 at a time (at 48 rows of 256 attn_kernel's three passes over
+// the cache took WIDE_OLD us a 100001-token request, the wide one WIDE_NEW); what is still
+// more goes in groups, each of which reads the cache again.
+struct Form {
+  bool wide;
+  int nt;
+};
+
+Form form_for(int D, int rows) {
+  const int want = (rows + 7) / 8;
+  if (D > 64 && want * D > 512) {
+    const int groups = (want + 7) / 8, each = (want + groups - 1) / groups;
+    return {true, each <= 4 && D == 256 ? 4 : each <= 6 ? 6 : 8};
+  }
   int nt = 1;
-  while (nt < want && nt < most) nt *= 2;
-  return nt;
+  while (nt < want && nt < 512 / D) nt *= 2;
+  return {false, nt};
 }
 
 template <int D, int NT>
 constexpr int attn_smem() { return Shape<D, NT>::kWarpBytes * kAttnWarps + (int)sizeof(Tail<D, NT>) + 1024; }
 
-int ctas_per_sm(int D, int nt) { return nt * D <= 128 ? 2 : 1; }   // Shape::kCtas
-
 struct AttnLayout {
-  size_t off_failed, off_ml, off_o, total;
-  int n_ctas, nt;
+  size_t off_cut, off_failed, off_ml, off_o, total;
+  int n_ctas;
+  Form form;
 };
 
 AttnLayout attn_layout(int H, int K, int D, int max_rows) {
   AttnLayout L;
-  L.nt = tiles_for(D, max_rows * (H / K));
-  L.n_ctas = num_sms() * ctas_per_sm(D, L.nt);
-  const size_t rows = (size_t)2 * L.n_ctas * 8 * L.nt;
+  L.form = form_for(D, max_rows * (H / K));
+  L.n_ctas = num_sms() * (L.form.nt * D <= 128 ? 2 : 1);   // Shape::kCtas
+  const size_t rows = (size_t)2 * L.n_ctas * 8 * L.form.nt;
   // bws_status_word reads 8 bytes here and eight words from 512 on
   size_t o = 1024;
+  L.off_cut = o; o += align256(2 * sizeof(int4) * (size_t)L.n_ctas);
   L.off_failed = o; o += align256(sizeof(uint32_t) * (size_t)L.n_ctas);
   L.off_ml = o; o += align256(sizeof(float2) * rows);
   L.off_o = o; o += align256(sizeof(float) * rows * D);
@@ -796,26 +610,33 @@ cudaError_t launch_attn(const AttnParams& p, cudaStream_t st) {
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_kernel<D, NT>, p);
-  if (e != cudaSuccess) return e;
-  const int rows = p.max_rows * p.G;
-  cfg.gridDim = dim3((unsigned)p.n_ctas, (unsigned)(rows < 8 * NT ? rows : 8 * NT));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, p);
+  return cudaLaunchKernelEx(&cfg, attn_kernel<D, NT>, p);
 }
 
 template <int D>
-cudaError_t launch_attn_d(int nt, const AttnParams& p, cudaStream_t st) {
-  if (nt == 1) return launch_attn<D, 1>(p, st);
-  if (nt == 2) return launch_attn<D, 2>(p, st);
+cudaError_t launch_attn_d(Form form, const AttnParams& p, cudaStream_t st) {
+  cudaError_t e = cudaErrorInvalidValue;
+  if (form.wide) e = launch_attn_wide(D, form.nt, p, st);
+  else if (form.nt == 1) e = launch_attn<D, 1>(p, st);
+  else if (form.nt == 2) e = launch_attn<D, 2>(p, st);
   if constexpr (D <= 128) {
-    if (nt == 4) return launch_attn<D, 4>(p, st);
+    if (!form.wide && form.nt == 4) e = launch_attn<D, 4>(p, st);
   }
   if constexpr (D <= 64) {
-    if (nt == 8) return launch_attn<D, 8>(p, st);
+    if (!form.wide && form.nt == 8) e = launch_attn<D, 8>(p, st);
   }
-  return cudaErrorInvalidValue;
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  const int rows = p.max_rows * p.G;
+  cfg.gridDim = dim3((unsigned)p.n_ctas, (unsigned)(rows < p.group_rows ? rows : p.group_rows));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
 }
 
 }  // namespace
@@ -866,10 +687,11 @@ int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_str
   char* w = static_cast<char*>(workspace);
   AttnParams p;
   memset(&p, 0, sizeof(p));
-  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)cache->block_tokens, (uint64_t)K, (uint64_t)cache->n_blocks};
-  const uint64_t strides[3] = {(uint64_t)D, cache->head_stride, cache->block_stride};
-  if (!encode_4d(&p.k, cache->k, dims, strides, D < 128 ? D : 128, kUnit) ||
-      !encode_4d(&p.v, cache->v, dims, strides, D < 128 ? D : 128, kUnit))
+  const uint32_t panel = D < 128 ? D : 128;
+  const uint64_t dims[5] = {panel, (uint64_t)cache->block_tokens, D / panel, (uint64_t)K, (uint64_t)cache->n_blocks};
+  const uint64_t strides[4] = {(uint64_t)D, panel, cache->head_stride, cache->block_stride};
+  const uint32_t box[5] = {panel, kBox, D / panel, 1, 1};
+  if (!encode_5d(&p.k, cache->k, dims, strides, box) || !encode_5d(&p.v, cache->v, dims, strides, box))
     return fail(BWS_ERR_CUDA, "%s: tensor map encoding failed", name);
   p.q = q;
   p.q_row_stride = q_row_stride;
@@ -892,17 +714,20 @@ int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_str
   p.out = out;
   p.lse = lse;
   p.hdr = reinterpret_cast<uint32_t*>(w);
+  p.cut = reinterpret_cast<int4*>(w + L.off_cut);
   p.failed = reinterpret_cast<uint32_t*>(w + L.off_failed);
   p.part_ml = reinterpret_cast<float2*>(w + L.off_ml);
   p.part_o = reinterpret_cast<float*>(w + L.off_o);
   p.n_ctas = L.n_ctas;
-  p.least = kAttnWarps;   // a unit for every warp
-  p.lead = 32;
+  p.group_rows = 8 * L.form.nt;
+  p.unit = L.form.wide ? kWideTile : kBox;
+  p.least = L.form.wide ? 1 : kAttnWarps;   // a box for every warp
+  p.lead = 32 * kBox / p.unit;              // 512 tokens: swept over a factor of 16, LEAD_NOTE
   cudaStream_t st = as_stream(stream);
   cudaError_t e;
-  if (D == 64) e = launch_attn_d<64>(L.nt, p, st);
-  else if (D == 128) e = launch_attn_d<128>(L.nt, p, st);
-  else e = launch_attn_d<256>(L.nt, p, st);
+  if (D == 64) e = launch_attn_d<64>(L.form, p, st);
+  else if (D == 128) e = launch_attn_d<128>(L.form, p, st);
+  else e = launch_attn_d<256>(L.form, p, st);
   return cuda_status(e, name);
 }
 

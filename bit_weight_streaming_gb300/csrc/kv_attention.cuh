@@ -1,0 +1,221 @@
+// Shared by the attention kernels over the 8-bit cache (kv_attention.cu for few
+// query rows, kv_attention_wide.cu for many): their parameters, the line of
+// shares, the shared-memory tiles.
+#pragma once
+#include <cuda.h>
+
+#include "bws_abi_util.h"
+#include "bws_common.cuh"
+#include "bws_internal.h"
+
+namespace bws {
+
+constexpr int kAttnWarps = 8;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kBox = 16;                   // cached tokens of a TMA box: never across a block
+constexpr int kAttnMaxRows = kMaxTokens;   // rows of a request
+constexpr int kAttnMaxGroup = 16;          // query heads of a kv head
+constexpr uint32_t kAttnPolls = 1u << 22;
+constexpr float kNone = -3.0e38f;           // a running maximum of nothing
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnParams {
+  CUtensorMap k, v;
+  const uint16_t* q;
+  long long q_row_stride, q_head_stride;
+  int n_rows, H, K, G;
+  int B, n_blocks;
+  const float *k_scale, *v_scale;
+  const int32_t* table;
+  int max_blocks, R;
+  const int32_t *row_start, *kv_lens;
+  int max_rows;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  float* part_o;      // [2 * CTAs][8 NT][D]
+  float2* part_ml;    // [2 * CTAs][8 NT]
+  int4* cut;          // [CTAs][2]: the segment that a CTA starts and others end
+  uint32_t* failed;   // [CTAs]
+  uint32_t* hdr;
+  int n_ctas, least;  // CTAs; smallest share in units
+  int lead;           // what a segment costs beside its units, in units
+  int unit;           // cached tokens of a unit
+  int group_rows;     // rows of a row group
+};
+
+// ---- the line of units -----------------------------------------------------------
+
+struct Request {
+  int rows, start, kv, units, groups;   // kv: cached tokens; units of one segment; row groups
+};
+
+BWS_DEV Request request_of(const AttnParams& p, int r, int group_rows) {
+  Request q;
+  q.start = min(max(p.row_start[r], 0), p.n_rows);
+  q.rows = min(max(p.row_start[r + 1] - q.start, 0), min(p.max_rows, p.n_rows - q.start));
+  const long long cap = (long long)p.max_blocks * p.B;
+  q.kv = (int)min((long long)max(p.kv_lens[r], 0), cap);
+  q.units = max(1, (q.kv + p.unit - 1) / p.unit);   // a request without tokens still writes its rows
+  q.groups = (q.rows * p.G + group_rows - 1) / group_rows;
+  return q;
+}
+
+BWS_DEV long long length_of(const AttnParams& p, const Request& q) {
+  return (long long)p.K * q.groups * (p.lead + q.units);
+}
+
+struct Line {
+  long long total, share;
+  int r;            // request that holds the asked position
+  long long base;   // its first position
+};
+
+// The whole CTA: the line's length, the share, and the request at position
+// cta * share, if the line has it.
+BWS_DEV Line find_on_line(const AttnParams& p, int group_rows, int cta, long long* s_warp, long long* s_found) {
+  const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.R + n - 1) / n;
+  const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += length_of(p, request_of(p, r, group_rows));
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += a;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  long long before = inc - mine, total = 0;
+  for (int w = 0; w < n / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  Line line;
+  line.total = total;
+  const long long share = (total + p.n_ctas - 1) / p.n_ctas;
+  line.share = share < p.least ? p.least : share;
+  const long long u = cta * line.share;
+  if (u >= before && u < before + mine) {
+    long long b = before;
+    int r = r0;
+    for (; r < r1 - 1; ++r) {
+      const long long k = length_of(p, request_of(p, r, group_rows));
+      if (u < b + k) break;
+      b += k;
+    }
+    s_found[0] = r;
+    s_found[1] = b;
+  }
+  __syncthreads();
+  line.r = (int)s_found[0];
+  line.base = s_found[1];
+  return line;
+}
+
+// One CTA's part of a segment: units [first, last).
+struct Segment {
+  Request rq;
+  int r, head, row0, first, last;
+  bool whole;      // the CTA has every unit
+  bool starts;     // the CTA has the first unit
+  int pieces;      // CTAs that have units, from the one that starts it on
+};
+
+// A CTA's way along its share, segment by segment.
+struct Walk {
+  long long u, u0, u1, base, share;
+  int r, cta;
+
+  BWS_DEV Walk(const AttnParams& p, int group_rows, long long* s_warp, long long* s_found) {
+    cta = blockIdx.x;
+    const Line line = find_on_line(p, group_rows, cta, s_warp, s_found);
+    share = line.share;
+    u = u0 = cta * share;
+    u1 = min(line.total, u0 + share);
+    base = line.base;
+    r = line.r;
+    if (threadIdx.x == 0) p.cut[2 * cta + 1] = make_int4(0, 0, 0, 0);
+  }
+  // The next segment that the share has units of; false: the share is done.
+  BWS_DEV bool next(const AttnParams& p, int group_rows, Segment& sg) {
+    while (u < u1) {
+      const Request rq = request_of(p, r, group_rows);
+      const long long rn = length_of(p, rq);
+      if (u >= base + rn) {
+        base += rn;
+        ++r;
+        continue;
+      }
+      const int len = p.lead + rq.units, seg = (int)((u - base) / len);
+      const long long a = base + (long long)seg * len, b = a + len, first_unit = a + p.lead;
+      const long long from = max(u, first_unit), to = min(u1, b);
+      u = to;
+      if (from >= to) continue;   // the share ends before the first unit
+      sg.rq = rq;
+      sg.r = r;
+      sg.head = seg / rq.groups;
+      sg.row0 = (seg % rq.groups) * group_rows;
+      sg.first = (int)(from - first_unit);
+      sg.last = (int)(to - first_unit);
+      sg.starts = first_unit >= u0;
+      sg.whole = sg.starts && to == b;
+      sg.pieces = sg.starts && !sg.whole ? (int)((b - 1) / share) - cta + 1 : 1;
+      if (sg.pieces > 1 && threadIdx.x == 0) {   // for the join
+        p.cut[2 * cta] = make_int4(rq.start, min(rq.rows * p.G - sg.row0, group_rows), sg.head, sg.row0);
+        p.cut[2 * cta + 1] = make_int4(sg.pieces, 0, 0, 0);
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+// ---- tiles ---------------------------------------------------------------------
+
+// A box of 16 tokens (from `token` of a block's head): all panels of 128 bytes of their rows, panel by panel.
+BWS_DEV void tma_load_box(uint32_t dst, const void* tmap, int token, int head, int block, uint32_t bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %2, %4, %5}], [%6], %7;"
+      :: "r"(dst), "l"(tmap), "r"(0), "r"(token), "r"(head), "r"(block), "r"(bar), "l"(pol) : "memory");
+}
+BWS_DEV void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+BWS_DEV void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+BWS_DEV uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+BWS_DEV uint2 lds_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+BWS_DEV float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+BWS_DEV void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Byte offset of 16-byte chunk `c` of token row `row` in a side.
+template <int D>
+BWS_DEV uint32_t chunk_at(int row, int c) {
+  if constexpr (D == 64) return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+  else return (c >> 3) * (kBox * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
+// kv_attention_wide.cu: nt tiles of 8 rows, 6 or 8, of 256 also 4.
+constexpr int kWideTile = 128;   // cached tokens of its unit
+cudaError_t launch_attn_wide(int D, int nt, const AttnParams& p, cudaStream_t st);
+
+}  // namespace bws

@@ -127,10 +127,9 @@ bool encode_fp4_2d(CUtensorMap* m, const void* base, uint64_t d_in, uint64_t row
 // n planes) with box {box_inner, box_rows, 1} and 128-byte swizzle.
 bool encode_3d(CUtensorMap* m, const void* base, uint64_t inner_bytes, uint64_t rows, uint64_t n,
                uint64_t stride2, uint32_t box_inner, uint32_t box_rows);
-// A 4D u8 tensor map of dims {inner, rows, n, m} (byte strides of the outer
-// three) with box {box_inner, box_rows, 1, 1}, box_inner 64 or 128, swizzled
-// over rows of that many bytes.
-bool encode_4d(CUtensorMap* m, const void* base, const uint64_t dims[4], const uint64_t strides[3],
-               uint32_t box_inner, uint32_t box_rows);
+// A 5D u8 tensor map of dims (byte strides of the outer four) with `box`,
+// box[0] 64 or 128, swizzled over rows of that many bytes.
+bool encode_5d(CUtensorMap* m, const void* base, const uint64_t dims[5], const uint64_t strides[4],
+               const uint32_t box[5]);
 
 }  // namespace bws
