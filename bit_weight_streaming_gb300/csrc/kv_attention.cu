@@ -51,7 +51,7 @@ struct Shape {
   static constexpr int kRing = kStages * kStage;
   static constexpr int kWarpBytes = kRing + (kOverlap ? kJoin : 0);
   static constexpr bool kQInRegs = NT * D <= 256;
-  static constexpr int kQStride = 2 * D + 16;                 // bytes of a query row, off the banks' period
+  static constexpr int kQStride = 2 * D + 32;                 // bytes of a query row: four rows of fragments on all banks
   static_assert(kStages >= 2 && (kOverlap || kRing >= kJoin), "ring");
 };
 
@@ -208,13 +208,13 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     uint32_t* const nan_mask = T.nan_mask[turn];
 
     uint32_t qf[S::kQInRegs ? kMT : 1][S::kQInRegs ? NT : 1][2];
-    const uint32_t q_at = smem_u32(T.q) + g * S::kQStride + t4 * 8;
+    const uint8_t* const q_frag = T.q + g * S::kQStride + t4 * 8;   // this lane's fragment of chunk 0, row g
     if constexpr (S::kQInRegs) {
 #pragma unroll
       for (int c = 0; c < kMT; ++c)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint2 b = lds_v2(q_at + n * 8 * S::kQStride + c * 32);
+          const uint2 b = *reinterpret_cast<const uint2*>(q_frag + n * 8 * S::kQStride + c * 32);
           qf[c][n][0] = b.x;
           qf[c][n][1] = b.y;
         }
@@ -286,11 +286,11 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
                 b0 = qf[c + h][n][0];
                 b1 = qf[c + h][n][1];
               } else {
-                const uint2 b = lds_v2(q_at + n * 8 * S::kQStride + (c + h) * 32);
+                const uint2 b = *reinterpret_cast<const uint2*>(q_frag + n * 8 * S::kQStride + (c + h) * 32);
                 b0 = b.x;
                 b1 = b.y;
               }
-              mma_f16_16816(acc[h % kChains][n], a0, a1, a2, a3, b0, b1);
+              mma_free(acc[h % kChains][n], a0, a1, a2, a3, b0, b1);
             }
           }
         }
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
             e4m3x4_to_f16x2x2(__byte_perm(w[2 * h], 0, 0x3120), a0, a1);
             e4m3x4_to_f16x2x2(__byte_perm(w[2 * h + 1], 0, 0x3120), a2, a3);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16_16816(o[c + h][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            for (int n = 0; n < NT; ++n) mma_free(o[c + h][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
           }
         }
       }
@@ -474,8 +474,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
   if (tid == 0) p.failed[cta] = T.failed;
 }
 
-// Joins the partial results of the segment that share x starts and does not
-// end; one row a CTA of the y axis, one float a thread.
+// Joins the partial results of a cut segment, x: its number where the segments
+// are fewer than the CTAs, else the CTA that starts it. One row a CTA of the y
+// axis, four floats a thread.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnParams p) {
   const int kRows = p.group_rows;
@@ -499,11 +500,16 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
     }
   }
   const int4 cut = p.cut[2 * c];
-  const int pieces = p.cut[2 * c + 1].x;
+  const int4 more = p.cut[2 * c + 1];
+  if (p.by_segment) {   // a request's missing row groups have no entry
+    const int r = c / (p.K * p.max_groups);
+    if (c % p.max_groups >= request_of(p, r, kRows).groups) return;
+  }
   const int n = blockIdx.y;
+  const int pieces = more.x, first = more.y;
   if (pieces < 2 || n >= cut.y) return;
   const int head = cut.z, row0 = cut.w;
-  auto slot_of = [&](int i) { return (c + i) * 2 + (i == 0 ? 1 : 0); };
+  auto slot_of = [&](int i) { return (first + i) * 2 + (i == 0 ? 1 : 0); };
   const int d4 = threadIdx.x % kLanes, at = threadIdx.x / kLanes;
   float top = kNone;
   for (int i = 0; i < pieces; ++i) top = fmaxf(top, p.part_ml[(size_t)slot_of(i) * kRows + n].x);
@@ -628,7 +634,8 @@ cudaError_t launch_attn_d(Form form, const AttnParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int rows = p.max_rows * p.G;
-  cfg.gridDim = dim3((unsigned)p.n_ctas, (unsigned)(rows < p.group_rows ? rows : p.group_rows));
+  cfg.gridDim = dim3((unsigned)(p.by_segment ? p.R * p.K * p.max_groups : p.n_ctas),
+                     (unsigned)(rows < p.group_rows ? rows : p.group_rows));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute a[1];
@@ -720,6 +727,8 @@ int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_str
   p.part_o = reinterpret_cast<float*>(w + L.off_o);
   p.n_ctas = L.n_ctas;
   p.group_rows = 8 * L.form.nt;
+  p.max_groups = (max_rows * p.G + p.group_rows - 1) / p.group_rows;
+  p.by_segment = (long long)n_requests * K * p.max_groups <= L.n_ctas;
   p.unit = L.form.wide ? kWideTile : kBox;
   p.least = L.form.wide ? 1 : kAttnWarps;   // a box for every warp
   p.lead = 32 * kBox / p.unit;              // 512 tokens: swept over a factor of 16, LEAD_NOTE

@@ -36,7 +36,9 @@ struct AttnParams {
   float* lse;
   float* part_o;      // [2 * CTAs][8 NT][D]
   float2* part_ml;    // [2 * CTAs][8 NT]
-  int4* cut;          // [CTAs][2]: the segment that a CTA starts and others end
+  int4* cut;          // [max(CTAs, segments)][2]: segments that other CTAs go on with
+  int by_segment;     // cut's index: the segment, else the CTA that starts it
+  int max_groups;     // row groups of a full request
   uint32_t* failed;   // [CTAs]
   uint32_t* hdr;
   int n_ctas, least;  // CTAs; smallest share in units
@@ -137,7 +139,7 @@ struct Walk {
     u1 = min(line.total, u0 + share);
     base = line.base;
     r = line.r;
-    if (threadIdx.x == 0) p.cut[2 * cta + 1] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0 && !p.by_segment) p.cut[2 * cta + 1] = make_int4(0, 0, 0, 0);
   }
   // The next segment that the share has units of; false: the share is done.
   BWS_DEV bool next(const AttnParams& p, int group_rows, Segment& sg) {
@@ -163,9 +165,10 @@ struct Walk {
       sg.starts = first_unit >= u0;
       sg.whole = sg.starts && to == b;
       sg.pieces = sg.starts && !sg.whole ? (int)((b - 1) / share) - cta + 1 : 1;
-      if (sg.pieces > 1 && threadIdx.x == 0) {   // for the join
-        p.cut[2 * cta] = make_int4(rq.start, min(rq.rows * p.G - sg.row0, group_rows), sg.head, sg.row0);
-        p.cut[2 * cta + 1] = make_int4(sg.pieces, 0, 0, 0);
+      if (sg.starts && threadIdx.x == 0 && (sg.pieces > 1 || p.by_segment)) {   // for the join
+        const int at = p.by_segment ? (r * p.K + sg.head) * p.max_groups + seg % rq.groups : cta;
+        p.cut[2 * at] = make_int4(rq.start, min(rq.rows * p.G - sg.row0, group_rows), sg.head, sg.row0);
+        p.cut[2 * at + 1] = make_int4(sg.pieces, cta, 0, 0);
       }
       return true;
     }
@@ -184,21 +187,22 @@ BWS_DEV void tma_load_box(uint32_t dst, const void* tmap, int token, int head, i
 }
 BWS_DEV void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 BWS_DEV void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+// mma_f16_16816 as a value of its operands alone: free to be scheduled.
+BWS_DEV void mma_free(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 BWS_DEV uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-BWS_DEV uint2 lds_v2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
 }
 BWS_DEV float exp2_fast(float x) {
   float y;

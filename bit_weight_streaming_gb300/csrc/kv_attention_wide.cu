@@ -26,7 +26,7 @@ struct Wide {
   static constexpr int kBoxBytes = kBox * D;                  // a warp's keys, or values, of a tile
   static constexpr int kSide = kAttnWarps * kBoxBytes;
   static constexpr int kStages = D == 256 ? 2 : 4;
-  static constexpr int kQStride = 2 * D + 16;                 // bytes of a query row, off the banks' period
+  static constexpr int kQStride = 2 * D + 32;                 // bytes of a query row: four rows of fragments on all banks
   static constexpr int kMT = D / 16 / kAttnWarps;             // m tiles of O^T a warp holds
   static constexpr int kPBytes = kAttnWarps * NT * 256;       // P of a tile, in fragments
 };
@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_wide_kernel(const __grid
     const int n_group_rows = min(rq.rows * p.G - row0, S::kRows);
     const int seen0 = rq.kv - rq.rows;   // row j sees tokens <= seen0 + j
     uint32_t* const nan_mask = T.nan_mask[turn];
-    const uint32_t q_at = smem_u32(T.q) + g * S::kQStride + t4 * 8, p_at = smem_u32(T.p);
+    const uint8_t* const q_frag = T.q + g * S::kQStride + t4 * 8;   // this lane's fragment of chunk 0, row g
+    const uint8_t* const p_frag = T.p + lane * 8;
     float qs[NT][2], m[NT][2], l[NT][2];
     float o[S::kMT][NT][4];
 #pragma unroll
@@ -233,21 +234,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_wide_kernel(const __grid
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[n][k] = there ? 0.0f : -INFINITY;
       if (there) {
+        // a chunk's query fragments and the next two chunks' keys are asked for
+        // before the chunk before is multiplied
+        uint2 qb[2][NT];
+        uint32_t w[2][4];
+        ldsm_x4(ks_at + chunk_at<D>(lrow, lchunk), w[0]);
 #pragma unroll
-        for (int c = 0; c < kChunks; c += 2) {
-          uint32_t w[4];
-          ldsm_x4(ks_at + chunk_at<D>(lrow, c + lchunk), w);
+        for (int n = 0; n < NT; ++n) qb[0][n] = *reinterpret_cast<const uint2*>(q_frag + n * 8 * S::kQStride);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t a0, a1, a2, a3;
-            e4m3x4_to_f16x2x2(w[2 * h], a0, a2);
-            e4m3x4_to_f16x2x2(w[2 * h + 1], a1, a3);
+        for (int c = 0; c < kChunks; ++c) {
+          if (c + 1 < kChunks) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint2 b = lds_v2(q_at + n * 8 * S::kQStride + (c + h) * 32);
-              mma_f16_16816(x[n], a0, a1, a2, a3, b.x, b.y);
-            }
+            for (int n = 0; n < NT; ++n)
+              qb[(c + 1) & 1][n] = *reinterpret_cast<const uint2*>(q_frag + n * 8 * S::kQStride + (c + 1) * 32);
           }
+          if (c % 2 == 0 && c + 2 < kChunks) ldsm_x4(ks_at + chunk_at<D>(lrow, c + 2 + lchunk), w[(c / 2 + 1) & 1]);
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x2x2(w[(c / 2) & 1][2 * (c & 1)], a0, a2);
+          e4m3x4_to_f16x2x2(w[(c / 2) & 1][2 * (c & 1) + 1], a1, a3);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_free(x[n], a0, a1, a2, a3, qb[c & 1][n].x, qb[c & 1][n].y);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -315,8 +321,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_wide_kernel(const __grid
         const __half2 h0 = __floats2half2_rn(wv[0], wv[1]), h1 = __floats2half2_rn(wv[2], wv[3]);
         const uint32_t b0 = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h0));
         const uint32_t b1 = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h1));
-        asm volatile("st.shared.v2.u32 [%0], {%1,%2};"
-                     :: "r"(p_at + (warp * NT + n) * 256 + lane * 8), "r"(b0), "r"(b1) : "memory");
+        *reinterpret_cast<uint2*>(T.p + (warp * NT + n) * 256 + lane * 8) = make_uint2(b0, b1);
       }
       if (!dead && !mbar_wait_bounded(v_bar + 8 * s, parity, kAttnPolls)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
@@ -348,31 +353,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_wide_kernel(const __grid
       }
       __syncthreads();   // ---- barrier 2: P is written
       // ---- O^T += V^T P^T over the tile's 128 tokens; m row g is dimension 2 g of a chunk, g + 8 is 2 g + 1
-#pragma unroll 2
-      for (int w = 0; w < kAttnWarps; w += 2 / S::kMT) {
-        // two chunks of one box, or one chunk of two boxes
-        uint32_t v[4];
-        const uint32_t at = S::kMT == 2 ? vs_at + w * S::kBoxBytes + chunk_at<D>(lrow, 2 * warp + lchunk)
-                                        : vs_at + (w + lchunk) * S::kBoxBytes + chunk_at<D>(lrow, warp);
-        ldsm_x4_t(at, v);
+      // (fragments of the next box asked for before a box is multiplied)
+      constexpr int kPer = 2 / S::kMT, kSteps = kAttnWarps / kPer;   // boxes a step: two chunks of one, or one of two
+      auto v_at = [&](int w) {
+        return S::kMT == 2 ? vs_at + w * S::kBoxBytes + chunk_at<D>(lrow, 2 * warp + lchunk)
+                           : vs_at + (w * kPer + lchunk) * S::kBoxBytes + chunk_at<D>(lrow, warp);
+      };
+      uint32_t v[2][4];
+      uint2 pb[2][NT];
+      ldsm_x4_t(v_at(0), v[0]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) pb[0][n] = *reinterpret_cast<const uint2*>(p_frag + n * 256);
+#pragma unroll
+      for (int w = 0; w < kSteps; ++w) {
+        if (w + 1 < kSteps) ldsm_x4_t(v_at(w + 1), v[(w + 1) & 1]);
         uint32_t a[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          e4m3x4_to_f16x2x2(__byte_perm(v[2 * h], 0, 0x3120), a[h][0], a[h][1]);
-          e4m3x4_to_f16x2x2(__byte_perm(v[2 * h + 1], 0, 0x3120), a[h][2], a[h][3]);
+          e4m3x4_to_f16x2x2(__byte_perm(v[w & 1][2 * h], 0, 0x3120), a[h][0], a[h][1]);
+          e4m3x4_to_f16x2x2(__byte_perm(v[w & 1][2 * h + 1], 0, 0x3120), a[h][2], a[h][3]);
         }
 #pragma unroll
-        for (int h = 0; h < 2 / S::kMT; ++h)
+        for (int h = 0; h < kPer; ++h) {
+          const int box = w * kPer + h;
+          if (box + 1 < kAttnWarps) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              pb[(box + 1) & 1][n] = *reinterpret_cast<const uint2*>(p_frag + ((box + 1) * NT + n) * 256);
+          }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint2 b = lds_v2(p_at + ((w + h) * NT + n) * 256 + lane * 8);
+            const uint2 b = pb[box & 1][n];
             if constexpr (S::kMT == 2) {
-              mma_f16_16816(o[0][n], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
-              mma_f16_16816(o[1][n], a[1][0], a[1][1], a[1][2], a[1][3], b.x, b.y);
+              mma_free(o[0][n], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
+              mma_free(o[1][n], a[1][0], a[1][1], a[1][2], a[1][3], b.x, b.y);
             } else {
-              mma_f16_16816(o[0][n], a[h][0], a[h][1], a[h][2], a[h][3], b.x, b.y);
+              mma_free(o[0][n], a[h][0], a[h][1], a[h][2], a[h][3], b.x, b.y);
             }
           }
+        }
       }
     }
     if (dead && lane == 0) {
