@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
   pdl_launch_dependents();
   pdl_wait();
   const int cta = blockIdx.x;
-  Walk walk(p, S::kRows, T.line_warp, T.line_found);
+  Walk walk;
+  walk.start(p, S::kRows, T.line_warp, T.line_found);
   const uint64_t pol = l2_evict_first();
   uint32_t phase_base = 0;   // units this warp has put through its ring
   bool dead = false;
@@ -584,7 +585,7 @@ struct AttnLayout {
 AttnLayout attn_layout(int H, int K, int D, int max_rows) {
   AttnLayout L;
   L.form = form_for(D, max_rows * (H / K));
-  L.n_ctas = num_sms() * (L.form.nt * D <= 128 ? 2 : 1);   // Shape::kCtas
+  L.n_ctas = num_sms() * (!L.form.wide && L.form.nt * D <= 128 ? 2 : 1);   // as their launch bounds ask
   const size_t rows = (size_t)2 * L.n_ctas * 8 * L.form.nt;
   // bws_status_word reads 8 bytes here and eight words from 512 on
   size_t o = 1024;
@@ -697,7 +698,7 @@ int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_str
   const uint32_t panel = D < 128 ? D : 128;
   const uint64_t dims[5] = {panel, (uint64_t)cache->block_tokens, D / panel, (uint64_t)K, (uint64_t)cache->n_blocks};
   const uint64_t strides[4] = {(uint64_t)D, panel, cache->head_stride, cache->block_stride};
-  const uint32_t box[5] = {panel, kBox, D / panel, 1, 1};
+  const uint32_t box[5] = {panel, kBox, L.form.wide ? 1 : D / panel, 1, 1};   // the wide kernel lays panels further apart
   if (!encode_5d(&p.k, cache->k, dims, strides, box) || !encode_5d(&p.v, cache->v, dims, strides, box))
     return fail(BWS_ERR_CUDA, "%s: tensor map encoding failed", name);
   p.q = q;

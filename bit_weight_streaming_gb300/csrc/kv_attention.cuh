@@ -131,7 +131,8 @@ struct Walk {
   long long u, u0, u1, base, share;
   int r, cta;
 
-  BWS_DEV Walk(const AttnParams& p, int group_rows, long long* s_warp, long long* s_found) {
+  // (the whole CTA)
+  BWS_DEV void start(const AttnParams& p, int group_rows, long long* s_warp, long long* s_found) {
     cta = blockIdx.x;
     const Line line = find_on_line(p, group_rows, cta, s_warp, s_found);
     share = line.share;

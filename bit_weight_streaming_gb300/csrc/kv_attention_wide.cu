@@ -2,17 +2,29 @@
 // of several tokens, wide groups): the mathematics and the line of shares are
 // those of kv_attention.cu, the CTA's work is cut the other way.
 //
-// With more than 16 rows of 256 (32 of 128) a warp cannot hold O for every
-// dimension, so here the eight warps share a tile of 128 cached tokens: for
-// S^T = K Q^T a warp takes 16 tokens and all rows, for O^T += V^T P^T an eighth
-// of the dimensions and all tokens. P crosses through shared memory in the
-// fragment order of the second product. One running maximum per row serves the
-// CTA: it follows only where an exponent passes it by more than 8, which the
-// barrier before P is written also votes on, so most tiles meet two barriers
-// and no exchange. Keys are a warp's own (its ring needs no barrier); values are
-// read by all, so their next copy waits for the tile's first barrier.
-// Bound: mma.sync (m16n8k16 takes 8 cycles of a quarter SM: 48 rows of 256 need
-// 3072 cycles a tile, of which HBM gives one in 2750), then shared memory.
+// mma.sync would set the time here: m16n8k16 keeps its pipe for 16 cycles of a
+// quarter SM, 67 us for both products of 48 rows of 256 over 100001 tokens, and
+// three arrangements of eight or sixteen warps all took 82 to 89 us. So the scores
+// go to the fifth-generation tensor cores, which take the keys as they are:
+// S^T = K Q^T as tcgen05.mma kind::f8f6f4 of M = 128 cached tokens, K's 128-byte
+// swizzled panels straight from TMA. A query row, scaled by a power of two to
+// 128..256 at its largest, is two E4M3 numbers, hi and 2^5 (q - hi): exact for
+// BF16 down to 2^-10 of the row's largest, off by 2^-23 of it below. Both stand
+// side by side in the N side (hi rows, then lo rows) and in TMEM, and are added
+// in FP32. The values' product stays on mma.sync in f16: weights in E4M3, of
+// however many parts on one scale, would drop what lies 2^-18 below a row's
+// largest, which over a long context can be a tenth of its sum.
+//
+// Roles, one CTA of sixteen warps an SM, along the tiles of 128 cached tokens:
+// warps 0-7 take a token and half the rows a thread (a TMEM lane's columns), form
+// the exponents and the weights P and copy the keys; warps 8-15 take an eighth of
+// the dimensions each and add V^T P^T to their registers, one of them also
+// issues the scores' products two tiles ahead and one copies the values.
+// mbarriers with bounded waits join them; a wait that runs out marks the result
+// and goes on. One running maximum per row serves the CTA: it follows only where
+// an exponent passes it by more than 8, on which warps 0-7 vote, so most tiles
+// exchange no maxima.
+// Bound: the values' mma.sync, then HBM. WIDE_FIGURES
 #include <atomic>
 
 #include "kv_attention.cuh"
@@ -20,438 +32,587 @@
 namespace bws {
 namespace {
 
+constexpr int kSoftWarps = 8, kValueWarps = 8, kQuads = 4;   // a quad: 32 tokens, two of warps 0-7
+constexpr int kMmaWarp = 6, kCopyWarp = 7;                   // of the value warps
+constexpr int kWideThreads = 32 * (kSoftWarps + kValueWarps);
+constexpr int kBoxes = kWideTile / kBox;
+constexpr int kTmemCols = 256;               // two buffers of 128 columns
+constexpr int kBarSoft = 1;                  // named barrier of warps 0-7
+constexpr float kLoScale = 1.0f / 32.0f;     // a query's low part is held times 2^5
+
 template <int D, int NT>
 struct Wide {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kBoxBytes = kBox * D;                  // a warp's keys, or values, of a tile
-  static constexpr int kSide = kAttnWarps * kBoxBytes;
+  static constexpr int kPanels = D / 128;
+  static constexpr int kPanel = kWideTile * 128;              // bytes: 128 tokens' 128 dimensions
+  static constexpr int kSide = kPanels * kPanel;              // a tile's keys, or values
+  static constexpr int kBoxBytes = kBox * D;
   static constexpr int kStages = D == 256 ? 2 : 4;
-  static constexpr int kQStride = 2 * D + 32;                 // bytes of a query row: four rows of fragments on all banks
-  static constexpr int kMT = D / 16 / kAttnWarps;             // m tiles of O^T a warp holds
-  static constexpr int kPBytes = kAttnWarps * NT * 256;       // P of a tile, in fragments
+  static constexpr int kQPanel = 2 * kRows * 128;             // hi rows, then lo rows
+  static constexpr int kPStride = 16 * NT + 16;               // bytes of a token's weights: eight tokens on all banks
+  static constexpr int kMT = D / 16 / kValueWarps;            // m tiles of O^T a value warp holds
+  // D FP32, A and B E4M3, both K-major, N = 2 kRows, M = 128
+  static constexpr uint32_t kIdesc = (1u << 4) | ((2u * kRows >> 3) << 17) | ((128u >> 4) << 24);
 };
 
 template <int D, int NT>
-struct __align__(16) WideTail {
-  uint8_t p[Wide<D, NT>::kPBytes];
-  uint8_t q[8 * NT * Wide<D, NT>::kQStride];
-  float q_scale[8 * NT];
-  float top[kAttnWarps][8 * NT];
-  float l[kAttnWarps][8 * NT];
+struct __align__(1024) WideTail {
+  uint8_t q[Wide<D, NT>::kPanels][Wide<D, NT>::kQPanel];      // swizzled as the keys are
+  uint8_t p[2][kWideTile * Wide<D, NT>::kPStride];
+  float2 row[8 * NT];          // scale (with log2 e and the row's power of two), running maximum or 0
+  uint32_t fresh[2];           // bit r: row r has seen no token yet, and its maximum stands for nothing
+  float up[8 * NT];            // how far the maxima went in a tile that moved them
+  float top[kQuads][8 * NT];
+  float l[kQuads][8 * NT];
+  float m[8 * NT];             // the segment's final maxima
+  float factor[2][8 * NT];     // what O shrinks by before the tile, where moved is set
+  uint32_t moved[2];
   uint32_t nan_mask[2][D];
-  unsigned long long k_full[kAttnWarps][Wide<D, NT>::kStages];
-  unsigned long long v_full[Wide<D, NT>::kStages];
-  long long line_warp[kAttnWarps];
+  unsigned long long k_full[Wide<D, NT>::kStages];
+  unsigned long long v_full[Wide<D, NT>::kStages], v_free[Wide<D, NT>::kStages];
+  unsigned long long s_full[2], p_full[2], p_free[2], drain;
+  long long line_warp[kSoftWarps + kValueWarps];
   long long line_found[2];
+  // the CTA's way along its share and its segments, kept here by thread 0
+  Walk walk;
+  Segment seg[2];
+  int more;
+  uint32_t tmem;
   uint32_t failed;
 };
 
 template <int D, int NT>
 constexpr int wide_smem() { return 2 * Wide<D, NT>::kStages * Wide<D, NT>::kSide + (int)sizeof(WideTail<D, NT>) + 1024; }
 
+// Shared-memory descriptor of a K-major operand of 128-byte swizzled rows.
+BWS_DEV uint64_t operand(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+BWS_DEV void mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+BWS_DEV void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+BWS_DEV void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+BWS_DEV void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+// This thread's lane of eight columns, twice (hi and lo of eight rows).
+BWS_DEV void load_scores(uint32_t hi_at, uint32_t lo_at, uint32_t (&a)[8], uint32_t (&b)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7])
+               : "r"(hi_at) : "memory");
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7])
+               : "r"(lo_at) : "memory");
+}
+BWS_DEV void wait_scores(uint32_t (&a)[8], uint32_t (&b)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+               :: "memory");
+}
+// A box of 16 tokens' panel of 128 dimensions.
+BWS_DEV void tma_load_panel(uint32_t dst, const void* tmap, int token, int panel, int head, int block, uint32_t bar,
+                            uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;"
+      :: "r"(dst), "l"(tmap), "r"(0), "r"(token), "r"(panel), "r"(head), "r"(block), "r"(bar), "l"(pol) : "memory");
+}
+// Byte offset of 16-byte chunk `c` of a token's row in a tile's side.
+BWS_DEV uint32_t tile_chunk_at(int token, int c) {
+  return (c >> 3) * (kWideTile * 128) + token * 128 + (((c & 7) ^ (token & 7)) << 4);
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, 1) attn_wide_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid_constant__ AttnParams p) {
   using S = Wide<D, NT>;
-  constexpr int kChunks = D / 16;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   unsigned char* const smem = smem_raw + (base - smem_u32(smem_raw));   // keys' stages, values' stages, tail
   WideTail<D, NT>& T = *reinterpret_cast<WideTail<D, NT>*>(smem + 2 * S::kStages * S::kSide);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t4 = lane & 3;
-  const uint32_t k_ring = base + warp * S::kBoxBytes, v_ring = base + S::kStages * S::kSide;
-  const uint32_t k_bar = smem_u32(&T.k_full[warp][0]), v_bar = smem_u32(&T.v_full[0]);
-  if (lane == 0)
-    for (int s = 0; s < S::kStages; ++s) mbar_init(k_bar + 8 * s, 1);
-  if (tid == 0) {
-    for (int s = 0; s < S::kStages; ++s) mbar_init(v_bar + 8 * s, kAttnWarps);
-    T.failed = 0;
+  const uint32_t k_ring = base, v_ring = base + S::kStages * S::kSide;
+  const uint32_t k_full = smem_u32(T.k_full), v_full = smem_u32(T.v_full), v_free = smem_u32(T.v_free),
+                 s_full = smem_u32(T.s_full), p_full = smem_u32(T.p_full), p_free = smem_u32(T.p_free);
+  const uint64_t pol = l2_evict_first();
+  if (warp == kSoftWarps + kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&T.tmem)),
+                 "n"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  mbar_fence_init();
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(k_full + 8 * s, kBoxes);
+      mbar_init(v_full + 8 * s, kBoxes);
+      mbar_init(v_free + 8 * s, kValueWarps);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(s_full + 8 * b, 1);
+      mbar_init(p_full + 8 * b, kSoftWarps);
+      mbar_init(p_free + 8 * b, kValueWarps);
+    }
+    mbar_init(smem_u32(&T.drain), 1);
+    T.failed = 0;
+    mbar_fence_init();
+  }
+  fence_before();
   pdl_launch_dependents();
   pdl_wait();
-  Walk walk(p, S::kRows, T.line_warp, T.line_found);   // its barriers publish the mbarriers too
-  const uint64_t pol = l2_evict_first();
-  uint32_t phase_base = 0;   // tiles put through the rings
-  bool dead = false;
-  // this lane's ldmatrix rows: tokens 0-7 and 8-15 of one chunk, then of the next
-  const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lchunk = lane >> 4;
-
-  Segment sg = {};
-  // ---- copies: this warp's 16 tokens of 32 tiles at a time, a tile a lane
-  int n_tiles = 0, ids = -1, toks = 0;
-  auto token_of = [&](int i) { return (sg.first + i) * kWideTile + warp * kBox; };
-  auto look_up = [&](int i, int& block, int& tok) {
+  {
+    Walk walk;
+    walk.start(p, S::kRows, T.line_warp, T.line_found);   // its barriers publish the mbarriers and the TMEM address too
+    if (tid == 0) {
+      T.walk = walk;
+      T.more = T.walk.next(p, S::kRows, T.seg[0]);
+    }
+  }
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = T.tmem;
+  uint32_t phase_base = 0;   // tiles gone by
+  bool dead = false;         // of this warp's lanes alike
+  int turn = 0;
+  // The (it / n)-th use of barrier it % n.
+  auto wait_for = [&](uint32_t bars, uint32_t it, int n, bool freed) {
+    const uint32_t use = it / n;
+    if (freed && use == 0) return;   // nothing was there before
+    if (!dead && !mbar_wait_bounded(bars + 8 * (it % n), (freed ? use - 1 : use) & 1, kAttnPolls)) dead = true;
+    dead = __any_sync(0xffffffffu, dead);
+  };
+  // Block and first token of box b of tile i of the segment; block -1: not there.
+  auto look_up = [&](int i, int b, int& block, int& tok) {
+    const Segment& sg = T.seg[turn];
     block = -1;
     tok = 0;
-    const int t = token_of(i);
-    if (i < n_tiles && t < sg.rq.kv) {
+    const int t = (sg.first + i) * kWideTile + b * kBox;
+    if (i < sg.last - sg.first && t < sg.rq.kv) {
       const int q = t / p.B;
-      const int b = p.table[(size_t)sg.r * p.max_blocks + q];
+      const int id = p.table[(size_t)sg.r * p.max_blocks + q];
       tok = t - q * p.B;
-      block = b >= 0 && b < p.n_blocks ? b : -1;
+      block = id >= 0 && id < p.n_blocks ? id : -1;
     }
   };
-  // Tile i's keys or values of this warp's tokens, by the whole warp. A batch is
-  // looked up with its first keys; the values of the batch before are all on
-  // their way by then.
-  auto issue = [&](int i, bool values) {
-    if (!values && (i & 31) == 0 && i > 0) look_up(i + lane, ids, toks);
-    const int b = __shfl_sync(0xffffffffu, ids, i & 31), tok = __shfl_sync(0xffffffffu, toks, i & 31);
-    if (lane == 0) {
-      const int s = (int)((phase_base + i) % S::kStages);
-      const uint32_t bar = (values ? v_bar : k_bar) + 8 * s;
-      const uint32_t dst = values ? v_ring + s * S::kSide + warp * S::kBoxBytes : k_ring + s * S::kSide;
-      if (b >= 0) {
-        mbar_arrive_expect_tx(bar, S::kBoxBytes);
-        tma_load_box(dst, values ? &p.v : &p.k, tok, sg.head, b, bar, pol);
-      } else {
-        mbar_arrive(bar);
-      }
-    }
-  };
-  struct Scales {
-    float ks, lvs, rvs;   // ks -1: the block is not there
-  };
-  Scales sc_l = {-1.0f, 0.0f, 0.0f}, sc_n = sc_l;
-  auto scales_of = [&](int b) {
-    Scales s = {-1.0f, 0.0f, 0.0f};
-    if (b >= 0) {
-      const size_t at = (size_t)b * p.K + sg.head;
-      s.ks = p.k_scale[at];
-      const float vs = fminf(fmaxf(p.v_scale[at], 0x1p-60f), 0x1p60f);
-      s.lvs = log2f(vs);
-      s.rvs = 1.0f / vs;
-    }
-    return s;
-  };
-  uint16_t qx[NT][D / 32];
-  auto open_segment = [&]() {
-    n_tiles = sg.last - sg.first;
-    look_up(lane, ids, toks);
+  // The segment's query rows as E4M3 pairs, a warp of 0-7 a row; clears a NaN mask.
+  auto store_queries = [&]() {
+    constexpr int E = D / 32;   // neighbouring values a lane
+    const Segment& sg = T.seg[turn];
     const int n_rows = min(sg.rq.rows * p.G - sg.row0, S::kRows);
+    uint2 raw[NT][E / 4];       // every row is asked for before the first is used
 #pragma unroll
-    for (int k = 0; k < NT; ++k) {
-      const int n = warp + k * kAttnWarps;
-      if (n < n_rows) {
-        const int j = (sg.row0 + n) / p.G, h = sg.head * p.G + (sg.row0 + n) % p.G;
-        const uint16_t* src = p.q + (sg.rq.start + j) * p.q_row_stride + h * p.q_head_stride + lane;
+    for (int r = 0; r < NT; ++r) {
+      const int n = warp + r * kSoftWarps;
+      const bool live = n < n_rows;
+      const int j = live ? (sg.row0 + n) / p.G : 0, h = sg.head * p.G + (live ? (sg.row0 + n) % p.G : 0);
+      const uint16_t* src = p.q + (sg.rq.start + j) * p.q_row_stride + h * p.q_head_stride + lane * E;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) qx[k][i] = src[32 * i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) qx[k][i] = 0;
-      }
+      for (int i = 0; i < E / 4; ++i) raw[r][i] = live ? *reinterpret_cast<const uint2*>(src + 4 * i) : make_uint2(0u, 0u);
     }
-    if (!dead) {
-      for (int i = 0; i < min(n_tiles, S::kStages); ++i) {
-        issue(i, false);
-        if (i < S::kStages - 1) issue(i, true);
-      }
-    }
-    sc_l = scales_of(ids);
-  };
-  // The query rows to f16, each scaled by a power of two; clears a NaN mask.
-  auto store_queries = [&](int slot) {
 #pragma unroll
-    for (int k = 0; k < NT; ++k) {
-      const int n = warp + k * kAttnWarps;
-      uint16_t* dst = reinterpret_cast<uint16_t*>(T.q + n * S::kQStride);
-      float x[D / 32];
+    for (int r = 0; r < NT; ++r) {
+      const int n = warp + r * kSoftWarps;
+      float x[E];
       float top = 0.0f;
+      bool bad = false;   // an infinity would saturate: a row that holds one is all NaN, as its scores are
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        x[i] = __uint_as_float((uint32_t)qx[k][i] << 16);
-        if (fabsf(x[i]) < INFINITY) top = fmaxf(top, fabsf(x[i]));
+      for (int i = 0; i < E / 4; ++i) {
+        x[4 * i] = __uint_as_float(raw[r][i].x << 16);
+        x[4 * i + 1] = __uint_as_float(raw[r][i].x & 0xFFFF0000u);
+        x[4 * i + 2] = __uint_as_float(raw[r][i].y << 16);
+        x[4 * i + 3] = __uint_as_float(raw[r][i].y & 0xFFFF0000u);
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        bad |= !(fabsf(x[i]) < INFINITY);
+        top = fmaxf(top, fabsf(x[i]));
       }
       top = warp_max(top);
-      const int e = top > 0.0f ? min(max(floor_log2_abs(top), -100), 126) : 0;
+      bad = __any_sync(0xffffffffu, bad);
+      const int e = top > 0.0f && !bad ? min(max(floor_log2_abs(top), -100), 126) - 7 : 0;
       const float f = exp2i(-e);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = __half_as_ushort(__float2half_rn(x[i] * f));
-      if (lane == 0) T.q_scale[n] = p.scale * kLog2e * exp2i(e);
+      for (int i = 0; i < E; i += 4) {
+        uint32_t hi = 0, lo = 0;
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const float a = x[i + k] * f, b = x[i + k + 1] * f;
+          const uint32_t h2 = f32x2_to_e4m3x2(b, a);
+          const uint32_t back = e4m3x2_to_f16x2(h2);
+          const float2 r2 = __half22float2(*reinterpret_cast<const __half2*>(&back));
+          hi |= h2 << (8 * k);
+          lo |= f32x2_to_e4m3x2((b - r2.y) * 32.0f, (a - r2.x) * 32.0f) << (8 * k);
+        }
+        if (bad) hi = lo = 0x7F7F7F7Fu;
+        const int d = lane * E + i, c = (d & 127) >> 4;
+        uint8_t* at = T.q[d >> 7] + n * 128 + ((c ^ (n & 7)) << 4) + (d & 15);
+        *reinterpret_cast<uint32_t*>(at) = hi;
+        *reinterpret_cast<uint32_t*>(at + S::kRows * 128) = lo;   // kRows is a multiple of 8: the same swizzle
+      }
+      if (lane == 0) T.row[n] = make_float2(p.scale * kLog2e * exp2i(e), 0.0f);
     }
-    for (int i = tid; i < D; i += kAttnThreads) T.nan_mask[slot][i] = 0;
+    for (int i = tid; i < D; i += 32 * kSoftWarps) T.nan_mask[turn][i] = 0;
+    if (tid < 2) T.fresh[tid] = S::kRows >= 32 * (tid + 1) ? 0xffffffffu : (1u << (S::kRows & 31)) - 1u;
+    proxy_fence();   // the tensor cores read the queries
+  };
+  // One lane's box (its block and first token) of a tile into stage s.
+  auto copy_box = [&](uint32_t bars, uint32_t ring, const CUtensorMap* map, int s, int b, int block, int tok) {
+    const uint32_t bar = bars + 8 * s, dst = ring + s * S::kSide + b * (kBox * 128);
+    if (block >= 0) {
+      mbar_arrive_expect_tx(bar, S::kBoxBytes);
+#pragma unroll
+      for (int x = 0; x < S::kPanels; ++x)
+        tma_load_panel(dst + x * S::kPanel, map, tok, x, T.seg[turn].head, block, bar, pol);
+    } else {
+      mbar_arrive(bar);
+    }
+  };
+  // The keys' copies: lanes 0 and 1 of a quad's first warp; the values': lanes 0-7 of a value warp.
+  const bool keys = warp < kQuads && lane < 2, values = warp == kSoftWarps + kCopyWarp && lane < kBoxes;
+  const int my_box = keys ? 2 * warp + lane : lane;
+  auto open_copies = [&]() {
+    const int ahead = min(T.seg[turn].last - T.seg[turn].first, S::kStages);
+    if (!dead && (keys || values)) {
+      int block[S::kStages], tok[S::kStages];
+#pragma unroll
+      for (int i = 0; i < S::kStages; ++i) look_up(i, my_box, block[i], tok[i]);
+#pragma unroll
+      for (int i = 0; i < S::kStages; ++i)
+        if (i < ahead)
+          copy_box(keys ? k_full : v_full, keys ? k_ring : v_ring, keys ? &p.k : &p.v,
+                   (int)((phase_base + i) % S::kStages), my_box, block[i], tok[i]);
+    }
+    __syncwarp();
   };
 
-  bool more = walk.next(p, S::kRows, sg);
-  int turn = 0;
+  bool more = T.more != 0;
   if (more) {
-    open_segment();
-    store_queries(0);
+    open_copies();
+    if (warp < kSoftWarps) store_queries();
   }
   while (more) {
     __syncthreads();
-    const Segment cur = sg;
+    const Segment& cur = T.seg[turn];
     const Request& rq = cur.rq;
-    const int row0 = cur.row0;
-    const int n_group_rows = min(rq.rows * p.G - row0, S::kRows);
+    const int tiles = cur.last - cur.first;
     const int seen0 = rq.kv - rq.rows;   // row j sees tokens <= seen0 + j
     uint32_t* const nan_mask = T.nan_mask[turn];
-    const uint8_t* const q_frag = T.q + g * S::kQStride + t4 * 8;   // this lane's fragment of chunk 0, row g
-    const uint8_t* const p_frag = T.p + lane * 8;
-    float qs[NT][2], m[NT][2], l[NT][2];
-    float o[S::kMT][NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        qs[n][k] = T.q_scale[n * 8 + t4 * 2 + k];
-        m[n][k] = kNone;
-        l[n][k] = 0.0f;
-      }
-#pragma unroll
-    for (int c = 0; c < S::kMT; ++c)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[c][n][k] = 0.0f;
+    float o[S::kMT][NT][4];              // the value warps'
+    const int g = lane >> 2, t4 = lane & 3;
 
-    const int tiles = n_tiles;
-    for (int i = 0; i < tiles; ++i) {
-      const uint32_t it = phase_base + i;
-      const int s = (int)(it % S::kStages), parity = (int)((it / S::kStages) & 1);
-      const uint32_t ks_at = k_ring + s * S::kSide, vs_at = v_ring + s * S::kSide;
-      const uint32_t v_own = vs_at + warp * S::kBoxBytes;
-      // A wait that runs out: the warp goes on without waiting or copying, in
-      // step with the barriers, and the result is reported as not valid.
-      if (!dead && !mbar_wait_bounded(k_bar + 8 * s, parity, kAttnPolls)) dead = true;
-      dead = __any_sync(0xffffffffu, dead);
-      if ((i & 31) == 16) {   // half a batch ahead
+    if (warp < kSoftWarps) {
+      // ---- a token and half the rows a thread: exponents and weights
+      constexpr int kHalf = 4 * NT;
+      const int quad = warp & 3, row_a = (warp >> 2) * kHalf, token = quad * 32 + lane;
+      float l[kHalf];    // this thread's tokens' sums
+#pragma unroll
+      for (int n = 0; n < kHalf; ++n) l[n] = 0.0f;
+      int k_block = -1, k_tok = 0;   // of the next keys to copy
+      if (keys) look_up(S::kStages, my_box, k_block, k_tok);
+      // the scales of this thread's box, asked for a tile ahead
+      auto scales_of = [&](int i, float& ks, float& vs) {
         int b, tok;
-        look_up((i & ~31) + 32 + lane, b, tok);
-        sc_n = scales_of(b);
-      }
-      if ((i & 31) == 0 && i > 0) sc_l = sc_n;
-      const float ks = __shfl_sync(0xffffffffu, sc_l.ks, i & 31), lvs = __shfl_sync(0xffffffffu, sc_l.lvs, i & 31),
-                  rvs = __shfl_sync(0xffffffffu, sc_l.rvs, i & 31);
-      const int tok0 = token_of(i);
-      const bool there = ks != -1.0f && !dead;
-      // ---- S^T: this warp's 16 tokens x rows, as exponents
-      float x[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[n][k] = there ? 0.0f : -INFINITY;
-      if (there) {
-        // a chunk's query fragments and the next two chunks' keys are asked for
-        // before the chunk before is multiplied
-        uint2 qb[2][NT];
-        uint32_t w[2][4];
-        ldsm_x4(ks_at + chunk_at<D>(lrow, lchunk), w[0]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) qb[0][n] = *reinterpret_cast<const uint2*>(q_frag + n * 8 * S::kQStride);
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          if (c + 1 < kChunks) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              qb[(c + 1) & 1][n] = *reinterpret_cast<const uint2*>(q_frag + n * 8 * S::kQStride + (c + 1) * 32);
-          }
-          if (c % 2 == 0 && c + 2 < kChunks) ldsm_x4(ks_at + chunk_at<D>(lrow, c + 2 + lchunk), w[(c / 2 + 1) & 1]);
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x2x2(w[(c / 2) & 1][2 * (c & 1)], a0, a2);
-          e4m3x4_to_f16x2x2(w[(c / 2) & 1][2 * (c & 1) + 1], a1, a3);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_free(x[n], a0, a1, a2, a3, qb[c & 1][n].x, qb[c & 1][n].y);
+        look_up(i, token / kBox, b, tok);
+        ks = -1.0f;   // the block is not there
+        vs = 1.0f;
+        if (b >= 0) {
+          const size_t at = (size_t)b * p.K + cur.head;
+          ks = p.k_scale[at];
+          vs = p.v_scale[at];
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[n][k] = fmaf(x[n][k], ks * qs[n][k & 1], lvs);
-      }
-      const bool ragged = !there || tok0 + kBox - 1 > seen0;   // some rows do not see all 16
-      if (ragged) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int lim = min(seen0 + (row0 + n * 8 + t4 * 2 + k) / p.G, rq.kv - 1);
-            if (tok0 + g > lim) x[n][k] = -INFINITY;
-            if (tok0 + g + 8 > lim) x[n][k + 2] = -INFINITY;
-          }
-      }
-      bool grew = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) grew |= x[n][k] > m[n][k & 1] + 8.0f;
-      // ---- barrier 1: the last tile's values and P are read, the keys are read
-      const bool move = __syncthreads_or(grew);
-      if (!dead) {
-        if (i + S::kStages - 1 < tiles) issue(i + S::kStages - 1, true);
-        if (i + S::kStages < tiles) issue(i + S::kStages, false);
-      }
-      if (move) {   // the same in every thread: new maxima, the same in every warp
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float v = fmaxf(x[n][k], x[n][k + 2]);
-#pragma unroll
-            for (int y = 4; y < 32; y <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, y));
-            if (g == 0) T.top[warp][n * 8 + t4 * 2 + k] = v;
-          }
-        __syncthreads();   // T.top is next written after another barrier 1
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float to = m[n][k];
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) to = fmaxf(to, T.top[w][n * 8 + t4 * 2 + k]);
-            const float f = exp2_fast(m[n][k] - to);
-            m[n][k] = to;
-            l[n][k] *= f;
-#pragma unroll
-            for (int c = 0; c < S::kMT; ++c) {
-              o[c][n][k] *= f;
-              o[c][n][k + 2] *= f;
-            }
-          }
-      }
-      // ---- weights and their sums; P in the fragments of the second product
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float wv[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) wv[k] = exp2_fast(x[n][k] - m[n][k & 1]);
-        l[n][0] = fmaf(wv[0] + wv[2], rvs, l[n][0]);
-        l[n][1] = fmaf(wv[1] + wv[3], rvs, l[n][1]);
-        const __half2 h0 = __floats2half2_rn(wv[0], wv[1]), h1 = __floats2half2_rn(wv[2], wv[3]);
-        const uint32_t b0 = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h0));
-        const uint32_t b1 = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h1));
-        *reinterpret_cast<uint2*>(T.p + (warp * NT + n) * 256 + lane * 8) = make_uint2(b0, b1);
-      }
-      if (!dead && !mbar_wait_bounded(v_bar + 8 * s, parity, kAttnPolls)) dead = true;
-      dead = __any_sync(0xffffffffu, dead);
-      if (ragged) {
-        // Values no row or not every row may see: rows past the end, or without
-        // a block, are zeroed (the memory may hold anything), and a NaN among the
-        // rows' own tokens is taken out here and put back at the end for the rows
-        // that do see it; 0 * NaN would reach the others.
-        __syncwarp();
-        for (int b = lane; b < kBox * (D / 4); b += 32) {
-          const int tk = b / (D / 4), byte = (b % (D / 4)) * 4, own = tok0 + tk - seen0;
-          if (there && own <= 0) continue;
-          const uint32_t at = v_own + chunk_at<D>(tk, byte >> 4) + (byte & 15);
-          uint32_t word;
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(word) : "r"(at) : "memory");
-          if (!there || tok0 + tk >= rq.kv) {
-            word = 0;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (((word >> (8 * k)) & 0x7Fu) == 0x7Fu) {
-                word &= ~(0xFFu << (8 * k));
-                atomicOr(&nan_mask[byte + k], 1u << own);
-              }
-          }
-          asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(word) : "memory");
-        }
-        proxy_fence();   // before TMA writes the stage again
-      }
-      __syncthreads();   // ---- barrier 2: P is written
-      // ---- O^T += V^T P^T over the tile's 128 tokens; m row g is dimension 2 g of a chunk, g + 8 is 2 g + 1
-      // (fragments of the next box asked for before a box is multiplied)
-      constexpr int kPer = 2 / S::kMT, kSteps = kAttnWarps / kPer;   // boxes a step: two chunks of one, or one of two
-      auto v_at = [&](int w) {
-        return S::kMT == 2 ? vs_at + w * S::kBoxBytes + chunk_at<D>(lrow, 2 * warp + lchunk)
-                           : vs_at + (w * kPer + lchunk) * S::kBoxBytes + chunk_at<D>(lrow, warp);
       };
-      uint32_t v[2][4];
-      uint2 pb[2][NT];
-      ldsm_x4_t(v_at(0), v[0]);
+      float ks_n, vs_n;
+      scales_of(0, ks_n, vs_n);
+      for (int i = 0; i < tiles; ++i) {
+        const uint32_t it = phase_base + i;
+        const int buf = (int)(it & 1);
+        const float ks = ks_n, vs = fminf(fmaxf(vs_n, 0x1p-60f), 0x1p60f);
+        scales_of(i + 1, ks_n, vs_n);
+        const float lvs = log2f(vs), rvs = 1.0f / vs;
+        const int tok = (cur.first + i) * kWideTile + token, own = tok - seen0;
+        const bool there = ks != -1.0f && tok < rq.kv;
+        // rows below `hidden` do not see the token: the j-th token of the rows'
+        // own is seen from row j on
+        const int hidden = !there ? S::kRows : own > 0 ? min(max(own * p.G - cur.row0, 0), S::kRows) : 0;
+        const bool ragged = __any_sync(0xffffffffu, !there || own > 0);
+        wait_for(s_full, it, 2, false);
+        if (keys && !dead && i + S::kStages < tiles)   // the products have read the keys
+          copy_box(k_full, k_ring, &p.k, (int)(it % S::kStages), my_box, k_block, k_tok);
+        if (keys) look_up(i + S::kStages + 1, my_box, k_block, k_tok);
+        __syncwarp();
+        fence_after();
+        const uint32_t s_at = tmem + buf * 128 + ((uint32_t)(32 * quad) << 16) + row_a;
+        const float2* const rows = T.row + row_a;
+        // exponents of every row, less the running maximum
+        float x[kHalf];
+        float top = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) pb[0][n] = *reinterpret_cast<const uint2*>(p_frag + n * 256);
+        for (int n = 0; n < kHalf; n += 8) {
+          uint32_t hi[8], lo[8];
+          load_scores(s_at + n, s_at + S::kRows + n, hi, lo);
+          wait_scores(hi, lo);
 #pragma unroll
-      for (int w = 0; w < kSteps; ++w) {
-        if (w + 1 < kSteps) ldsm_x4_t(v_at(w + 1), v[(w + 1) & 1]);
-        uint32_t a[2][4];
+          for (int k = 0; k < 8; ++k) {
+            const float2 row = rows[n + k];
+            x[n + k] = fmaf(fmaf(__uint_as_float(lo[k]), kLoScale, __uint_as_float(hi[k])), ks * row.x, lvs - row.y);
+          }
+        }
+        fence_before();
+        if (ragged) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          e4m3x4_to_f16x2x2(__byte_perm(v[w & 1][2 * h], 0, 0x3120), a[h][0], a[h][1]);
-          e4m3x4_to_f16x2x2(__byte_perm(v[w & 1][2 * h + 1], 0, 0x3120), a[h][2], a[h][3]);
+          for (int n = 0; n < kHalf; ++n)
+            if (row_a + n < hidden) x[n] = -INFINITY;
         }
 #pragma unroll
-        for (int h = 0; h < kPer; ++h) {
-          const int box = w * kPer + h;
-          if (box + 1 < kAttnWarps) {
+        for (int n = 0; n < kHalf; ++n) top = fmaxf(top, x[n]);
+        const bool grew = top > 8.0f || ((T.fresh[0] | T.fresh[1]) != 0u && top != -INFINITY);
+        uint32_t any;
+        asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, %2, %3, p; selp.u32 %0, 1, 0, q; }"
+                     : "=r"(any) : "r"((uint32_t)grew), "n"(kBarSoft), "n"(32 * kSoftWarps) : "memory");
+        wait_for(p_free, it, 2, true);   // the value warps are done with P and the factors of the tile before last
+        if (any != 0u) {                 // new maxima
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              pb[(box + 1) & 1][n] = *reinterpret_cast<const uint2*>(p_frag + ((box + 1) * NT + n) * 256);
+          for (int n = 0; n < kHalf; ++n) {
+            const float v = warp_max(x[n]);
+            if (lane == n) T.top[quad][row_a + n] = v;
           }
+          named_bar_sync(kBarSoft, 32 * kSoftWarps);
+          if (tid < 64) {
+            const bool row = tid < S::kRows, fresh = row && ((T.fresh[warp] >> lane) & 1u) != 0u;
+            float up = -INFINITY;
+            if (row)
+              for (int w = 0; w < kQuads; ++w) up = fmaxf(up, T.top[w][tid]);
+            const bool still = fresh && up == -INFINITY;
+            if (!fresh || still) up = fmaxf(up, 0.0f);
+            if (row) {
+              T.row[tid].y += up;
+              T.up[tid] = up;
+              T.factor[buf][tid] = fresh ? 1.0f : exp2_fast(-up);   // a fresh row's O and sum are 0
+            }
+            const unsigned left = __ballot_sync(0xffffffffu, still);
+            if (lane == 0) T.fresh[warp] = left;
+          }
+          named_bar_sync(kBarSoft, 32 * kSoftWarps);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint2 b = pb[box & 1][n];
-            if constexpr (S::kMT == 2) {
-              mma_free(o[0][n], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
-              mma_free(o[1][n], a[1][0], a[1][1], a[1][2], a[1][3], b.x, b.y);
-            } else {
-              mma_free(o[0][n], a[h][0], a[h][1], a[h][2], a[h][3], b.x, b.y);
+          for (int n = 0; n < kHalf; ++n) {
+            x[n] -= T.up[row_a + n];
+            l[n] *= T.factor[buf][row_a + n];
+          }
+        }
+        if (tid == 0) T.moved[buf] = any;
+        uint8_t* const p_row = T.p[buf] + token * S::kPStride + 2 * row_a;
+#pragma unroll
+        for (int n = 0; n < kHalf; n += 8) {
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            const float a = exp2_fast(x[n + k]), b = exp2_fast(x[n + k + 1]);
+            l[n + k] = fmaf(a, rvs, l[n + k]);
+            l[n + k + 1] = fmaf(b, rvs, l[n + k + 1]);
+            const __half2 h2 = __floats2half2_rn(a, b);
+            h[k / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          *reinterpret_cast<uint4*>(p_row + 2 * n) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        if (ragged) {
+          // Values no row or not every row may see: rows past the end, or without
+          // a block, are zeroed (the memory may hold anything), and a NaN among
+          // the rows' own tokens is taken out here and put back at the end for
+          // the rows that do see it; 0 * NaN would reach the others.
+          wait_for(v_full, it, S::kStages, false);
+          const uint32_t side = v_ring + (uint32_t)(it % S::kStages) * S::kSide;
+          // the quad's two warps take its tokens in turn, a word a lane
+          unsigned todo = __ballot_sync(0xffffffffu, !there || own > 0);
+          const unsigned live = __ballot_sync(0xffffffffu, there);
+          todo &= warp < kQuads ? 0x55555555u : 0xAAAAAAAAu;
+          while (todo != 0u) {
+            const int tk = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int its = (cur.first + i) * kWideTile + quad * 32 + tk - seen0;
+#pragma unroll
+            for (int byte = 4 * lane; byte < D; byte += 128) {
+              const uint32_t at = side + tile_chunk_at(quad * 32 + tk, byte >> 4) + (byte & 15);
+              uint32_t word = 0;
+              if ((live >> tk) & 1u) {
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(word) : "r"(at) : "memory");
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (((word >> (8 * k)) & 0x7Fu) == 0x7Fu) {
+                    word &= ~(0xFFu << (8 * k));
+                    atomicOr(&nan_mask[byte + k], 1u << its);
+                  }
+              }
+              asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(word) : "memory");
             }
           }
+          proxy_fence();   // before TMA writes the stage again
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * buf);
+      }
+#pragma unroll
+      for (int n = 0; n < kHalf; ++n) {
+        const float v = warp_sum(l[n]);
+        if (lane == n) T.l[quad][row_a + n] = v;
+      }
+      if (tid < S::kRows) T.m[tid] = ((T.fresh[warp] >> lane) & 1u) != 0u ? kNone : T.row[tid].y;
+    } else {
+      // ---- O^T += V^T P^T, an eighth of the dimensions; m row g is dimension 2 g
+      // of a chunk, g + 8 is 2 g + 1
+      const int vw = warp - kSoftWarps;
+      const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lhalf = lane >> 4;   // this lane's ldmatrix row
+#pragma unroll
+      for (int c = 0; c < S::kMT; ++c)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[c][n][k] = 0.0f;
+      auto score = [&](int i) {   // the whole warp: tile i's scores into their buffer, which is free
+        const uint32_t it = phase_base + i;
+        wait_for(k_full, it, S::kStages, false);
+        if (!dead && lane == 0) {
+          fence_after();
+          const uint32_t d = tmem + (it & 1) * 128, keys_at = k_ring + (it % S::kStages) * S::kSide;
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            mma_scores(d, operand(keys_at + (k >> 2) * S::kPanel + (k & 3) * 32),
+                       operand(smem_u32(T.q[k >> 2]) + (k & 3) * 32), S::kIdesc, k > 0);
+          commit(s_full + 8 * (it & 1));
+        }
+        __syncwarp();
+      };
+      if (vw == kMmaWarp)
+        for (int i = 0; i < min(tiles, 2); ++i) score(i);
+      for (int i = 0; i < tiles; ++i) {
+        const uint32_t it = phase_base + i;
+        const int s = (int)(it % S::kStages), buf = (int)(it & 1);
+        wait_for(p_full, it, 2, false);
+        if (vw == kMmaWarp && i + 2 < tiles) score(i + 2);   // P is there: its scores are read
+        wait_for(v_full, it, S::kStages, false);
+        if (T.moved[buf] != 0u) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float f = T.factor[buf][n * 8 + t4 * 2 + k];
+#pragma unroll
+              for (int c = 0; c < S::kMT; ++c) {
+                o[c][n][k] *= f;
+                o[c][n][k + 2] *= f;
+              }
+            }
+        }
+        const uint32_t vs_at = v_ring + s * S::kSide;
+        const uint32_t p_at = smem_u32(T.p[buf]) + lrow * S::kPStride + lhalf * 16;
+        constexpr int kPer = 2 / S::kMT;   // boxes a step: two chunks of one, or one of two
+#pragma unroll
+        for (int w = 0; w < kBoxes; w += kPer) {
+          uint32_t v[4];
+          ldsm_x4_t(vs_at + (S::kMT == 2 ? tile_chunk_at(w * kBox + lrow, 2 * vw + lhalf)
+                                         : tile_chunk_at((w + lhalf) * kBox + lrow, vw)), v);
+          uint32_t a[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            e4m3x4_to_f16x2x2(__byte_perm(v[2 * h], 0, 0x3120), a[h][0], a[h][1]);
+            e4m3x4_to_f16x2x2(__byte_perm(v[2 * h + 1], 0, 0x3120), a[h][2], a[h][3]);
+          }
+#pragma unroll
+          for (int h = 0; h < kPer; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+              uint32_t b[4];   // fragments of two tiles of rows
+              ldsm_x4_t(p_at + (w + h) * kBox * S::kPStride + n * 16, b);
+              if constexpr (S::kMT == 2) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  mma_free(o[c][n], a[c][0], a[c][1], a[c][2], a[c][3], b[0], b[1]);
+                  mma_free(o[c][n + 1], a[c][0], a[c][1], a[c][2], a[c][3], b[2], b[3]);
+                }
+              } else {
+                mma_free(o[0][n], a[h][0], a[h][1], a[h][2], a[h][3], b[0], b[1]);
+                mma_free(o[0][n + 1], a[h][0], a[h][1], a[h][2], a[h][3], b[2], b[3]);
+              }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(v_free + 8 * s);
+          mbar_arrive(p_free + 8 * buf);
+        }
+        if (vw == kCopyWarp && i + S::kStages < tiles) {
+          int block, tok;
+          look_up(i + S::kStages, my_box, block, tok);
+          wait_for(v_free, it + S::kStages, S::kStages, true);
+          if (values && !dead) copy_box(v_full, v_ring, &p.v, s, my_box, block, tok);
+          __syncwarp();
         }
       }
     }
     if (dead && lane == 0) {
       T.failed = 1;
       for (int s = 0; s < S::kStages; ++s) {   // the copies still on their way
-        mbar_wait_bounded(k_bar + 8 * s, (int)((phase_base / S::kStages) & 1), kAttnPolls);
-        mbar_wait_bounded(v_bar + 8 * s, (int)((phase_base / S::kStages) & 1), kAttnPolls);
+        mbar_wait_bounded(k_full + 8 * s, (int)((phase_base / S::kStages) & 1), kAttnPolls);
+        mbar_wait_bounded(v_full + 8 * s, (int)((phase_base / S::kStages) & 1), kAttnPolls);
       }
     }
     phase_base += tiles;
+    if (tid == 0) T.more = T.walk.next(p, S::kRows, T.seg[turn ^ 1]);
+    __syncthreads();   // the rows' sums and maxima, and the next segment, are there
 
-    // ---- the segment's end: the warps' sums, then each its dimensions
+    // ---- the segment's end, and the next one's start
+    more = T.more != 0;
+    turn ^= 1;
+    if (more) open_copies();
+    if (warp < kSoftWarps) {
+      if (more) store_queries();
+    } else {
+      const int vw = warp - kSoftWarps, row0 = cur.row0, n_group_rows = min(rq.rows * p.G - row0, S::kRows);
+      const int slot = blockIdx.x * 2 + (cur.starts ? 1 : 0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 2; ++k) {
+          const int row = n * 8 + t4 * 2 + k;
+          if (row >= n_group_rows) continue;
+          float sum = 0.0f;
 #pragma unroll
-        for (int y = 4; y < 32; y <<= 1) l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], y);
-        if (g == 0) T.l[warp][n * 8 + t4 * 2 + k] = l[n][k];
-      }
-    __syncthreads();
-    more = walk.next(p, S::kRows, sg);
-    if (more) {
-      open_segment();
-      store_queries(turn ^ 1);
-    }
-    const int slot = walk.cta * 2 + (cur.starts ? 1 : 0);
+          for (int w = 0; w < kQuads; ++w) sum += T.l[w][row];
+          const int j = (row0 + row) / p.G, h = cur.head * p.G + (row0 + row) % p.G;
+          const size_t at = (size_t)(rq.start + j) * p.H + h;
+          const uint32_t see = (2u << j) - 1u;
+          const float inv = cur.whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int row = n * 8 + t4 * 2 + k;
-        if (row >= n_group_rows) continue;
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) sum += T.l[w][row];
-        const int j = (row0 + row) / p.G, h = cur.head * p.G + (row0 + row) % p.G;
-        const size_t at = (size_t)(rq.start + j) * p.H + h;
-        const uint32_t see = (2u << j) - 1u;
-        const float inv = cur.whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-#pragma unroll
-        for (int c = 0; c < S::kMT; ++c) {
-          const int d = (warp * S::kMT + c) * 16 + 2 * g;
-          const float a = (nan_mask[d] & see) ? NAN : o[c][n][k] * inv, b = (nan_mask[d + 1] & see) ? NAN : o[c][n][k + 2] * inv;
-          if (cur.whole) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-            *reinterpret_cast<uint32_t*>(p.out + at * D + d) = *reinterpret_cast<const uint32_t*>(&v);
-          } else {
-            *reinterpret_cast<float2*>(p.part_o + ((size_t)slot * S::kRows + row) * D + d) = make_float2(a, b);
+          for (int c = 0; c < S::kMT; ++c) {
+            const int d = (vw * S::kMT + c) * 16 + 2 * g;
+            const float a = (nan_mask[d] & see) ? NAN : o[c][n][k] * inv;
+            const float b = (nan_mask[d + 1] & see) ? NAN : o[c][n][k + 2] * inv;
+            if (cur.whole) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+              *reinterpret_cast<uint32_t*>(p.out + at * D + d) = *reinterpret_cast<const uint32_t*>(&v);
+            } else {
+              *reinterpret_cast<float2*>(p.part_o + ((size_t)slot * S::kRows + row) * D + d) = make_float2(a, b);
+            }
+          }
+          if (vw == 0 && g == 0) {
+            if (!cur.whole) p.part_ml[(size_t)slot * S::kRows + row] = make_float2(T.m[row], sum);
+            else if (p.lse != nullptr) p.lse[at] = sum == 0.0f ? -INFINITY : (T.m[row] + log2f(sum)) * kLn2;
           }
         }
-        if (warp == 0 && g == 0) {
-          if (!cur.whole) p.part_ml[(size_t)slot * S::kRows + row] = make_float2(m[n][k], sum);
-          else if (p.lse != nullptr) p.lse[at] = sum == 0.0f ? -INFINITY : (m[n][k] + log2f(sum)) * kLn2;
-        }
-      }
-    turn ^= 1;
+    }
   }
   __syncthreads();
-  if (tid == 0) p.failed[walk.cta] = T.failed;
+  if (tid == 0) p.failed[blockIdx.x] = T.failed;
+  if (warp == kSoftWarps + kMmaWarp) {   // every product has finished before the columns are released
+    if (lane == 0) {
+      commit(smem_u32(&T.drain));
+      mbar_wait_bounded(smem_u32(&T.drain), 0, kAttnPolls);
+    }
+    __syncwarp();
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
+  }
 }
 
 template <int D, int NT>
@@ -461,7 +622,7 @@ cudaError_t launch_wide(const AttnParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.n_ctas);
-  cfg.blockDim = dim3(kAttnThreads);
+  cfg.blockDim = dim3(kWideThreads);
   cfg.dynamicSmemBytes = wide_smem<D, NT>();
   cfg.stream = st;
   cudaLaunchAttribute a[1];
