@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     tok = 0;
     const int t = token_of(i);
     if (i < mine && t < sg.rq.kv) {
-      const int q = t / p.B;
+      const int q = block_index(p, t);
       const int b = p.table[(size_t)sg.r * p.max_blocks + q];
       tok = t - q * p.B;
       block = b >= 0 && b < p.n_blocks ? b : -1;
@@ -709,6 +709,8 @@ int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_str
   p.K = K;
   p.G = n_q_heads / K;
   p.B = cache->block_tokens;
+  const uint32_t boxes = (uint32_t)p.B / kBox;
+  p.b_inverse = boxes == 1 ? 0u : (uint32_t)(((1ull << 32) + boxes - 1) / boxes);
   p.n_blocks = cache->n_blocks;
   p.k_scale = cache->k_scale;
   p.v_scale = cache->v_scale;

@@ -15,7 +15,7 @@ constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kBox = 16;                   // cached tokens of a TMA box: never across a block
 constexpr int kAttnMaxRows = kMaxTokens;   // rows of a request
 constexpr int kAttnMaxGroup = 16;          // query heads of a kv head
-constexpr uint32_t kAttnPolls = 1u << 22;
+constexpr uint32_t kAttnPolls = 1u << 20;
 constexpr float kNone = -3.0e38f;           // a running maximum of nothing
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -26,6 +26,7 @@ struct AttnParams {
   long long q_row_stride, q_head_stride;
   int n_rows, H, K, G;
   int B, n_blocks;
+  uint32_t b_inverse; // ceil(2^32 / (B / 16)), 0 for B = 16
   const float *k_scale, *v_scale;
   const int32_t* table;
   int max_blocks, R;
@@ -48,6 +49,12 @@ struct AttnParams {
 };
 
 // ---- the line of units -----------------------------------------------------------
+
+// token / B, exactly: in units of 16 the quotient's error, below 16 * 2^27 / 2^32, never reaches the next whole.
+BWS_DEV int block_index(const AttnParams& p, int token) {
+  const uint32_t t = (uint32_t)token >> 4;
+  return (int)(p.b_inverse != 0u ? __umulhi(t, p.b_inverse) : t);
+}
 
 struct Request {
   int rows, start, kv, units, groups;   // kv: cached tokens; units of one segment; row groups

@@ -17,9 +17,10 @@
 //
 // Roles, one CTA of sixteen warps an SM, along the tiles of 128 cached tokens:
 // warps 0-7 take a token and half the rows a thread (a TMEM lane's columns), form
-// the exponents and the weights P and copy the keys; warps 8-15 take an eighth of
+// the exponents and the weights P; warps 8-15 take an eighth of
 // the dimensions each and add V^T P^T to their registers, one of them also
-// issues the scores' products two tiles ahead and one copies the values.
+// issues the scores' products two tiles ahead, and each copies a box of keys and
+// values.
 // mbarriers with bounded waits join them; a wait that runs out marks the result
 // and goes on. One running maximum per row serves the CTA: it follows only where
 // an exponent passes it by more than 8, on which warps 0-7 vote, so most tiles
@@ -33,7 +34,7 @@ namespace bws {
 namespace {
 
 constexpr int kSoftWarps = 8, kValueWarps = 8, kQuads = 4;   // a quad: 32 tokens, two of warps 0-7
-constexpr int kMmaWarp = 6, kCopyWarp = 7;                   // of the value warps
+constexpr int kMmaWarp = 7;                                  // of the value warps
 constexpr int kWideThreads = 32 * (kSoftWarps + kValueWarps);
 constexpr int kBoxes = kWideTile / kBox;
 constexpr int kTmemCols = 256;               // two buffers of 128 columns
@@ -47,7 +48,10 @@ struct Wide {
   static constexpr int kPanel = kWideTile * 128;              // bytes: 128 tokens' 128 dimensions
   static constexpr int kSide = kPanels * kPanel;              // a tile's keys, or values
   static constexpr int kBoxBytes = kBox * D;
-  static constexpr int kStages = D == 256 ? 2 : 4;
+  // Keys are scored two tiles ahead of their weights' use, so a stage more of
+  // them keeps HBM's latency off that chain (eight tiles of rows leave no room).
+  static constexpr int kVStages = D == 256 ? 2 : 4;
+  static constexpr int kKStages = D == 256 ? (NT <= 6 ? 3 : 2) : 4;
   static constexpr int kQPanel = 2 * kRows * 128;             // hi rows, then lo rows
   static constexpr int kPStride = 16 * NT + 16;               // bytes of a token's weights: eight tokens on all banks
   static constexpr int kMT = D / 16 / kValueWarps;            // m tiles of O^T a value warp holds
@@ -59,7 +63,7 @@ template <int D, int NT>
 struct __align__(1024) WideTail {
   uint8_t q[Wide<D, NT>::kPanels][Wide<D, NT>::kQPanel];      // swizzled as the keys are
   uint8_t p[2][kWideTile * Wide<D, NT>::kPStride];
-  float2 row[8 * NT];          // scale (with log2 e and the row's power of two), running maximum or 0
+  alignas(16) float2 row[8 * NT];   // scale (with log2 e and the row's power of two), running maximum or 0
   uint32_t fresh[2];           // bit r: row r has seen no token yet, and its maximum stands for nothing
   float up[8 * NT];            // how far the maxima went in a tile that moved them
   float top[kQuads][8 * NT];
@@ -68,8 +72,8 @@ struct __align__(1024) WideTail {
   float factor[2][8 * NT];     // what O shrinks by before the tile, where moved is set
   uint32_t moved[2];
   uint32_t nan_mask[2][D];
-  unsigned long long k_full[Wide<D, NT>::kStages];
-  unsigned long long v_full[Wide<D, NT>::kStages], v_free[Wide<D, NT>::kStages];
+  unsigned long long k_full[Wide<D, NT>::kKStages], k_free[Wide<D, NT>::kKStages];
+  unsigned long long v_full[Wide<D, NT>::kVStages], v_free[Wide<D, NT>::kVStages];
   unsigned long long s_full[2], p_full[2], p_free[2], drain;
   long long line_warp[kSoftWarps + kValueWarps];
   long long line_found[2];
@@ -82,7 +86,7 @@ struct __align__(1024) WideTail {
 };
 
 template <int D, int NT>
-constexpr int wide_smem() { return 2 * Wide<D, NT>::kStages * Wide<D, NT>::kSide + (int)sizeof(WideTail<D, NT>) + 1024; }
+constexpr int wide_smem() { return (Wide<D, NT>::kKStages + Wide<D, NT>::kVStages) * Wide<D, NT>::kSide + (int)sizeof(WideTail<D, NT>) + 1024; }
 
 // Shared-memory descriptor of a K-major operand of 128-byte swizzled rows.
 BWS_DEV uint64_t operand(uint32_t addr) {
@@ -100,7 +104,7 @@ BWS_DEV void commit(uint32_t bar) {
 BWS_DEV void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 BWS_DEV void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 // This thread's lane of eight columns, twice (hi and lo of eight rows).
-BWS_DEV void load_scores(uint32_t hi_at, uint32_t lo_at, uint32_t (&a)[8], uint32_t (&b)[8]) {
+BWS_DEV void load_scores(uint32_t hi_at, uint32_t lo_at, uint32_t* a, uint32_t* b) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7])
                : "r"(hi_at) : "memory");
@@ -108,7 +112,7 @@ BWS_DEV void load_scores(uint32_t hi_at, uint32_t lo_at, uint32_t (&a)[8], uint3
                : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7])
                : "r"(lo_at) : "memory");
 }
-BWS_DEV void wait_scores(uint32_t (&a)[8], uint32_t (&b)[8]) {
+BWS_DEV void wait_scores(uint32_t* a, uint32_t* b) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
                  "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
@@ -133,10 +137,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   unsigned char* const smem = smem_raw + (base - smem_u32(smem_raw));   // keys' stages, values' stages, tail
-  WideTail<D, NT>& T = *reinterpret_cast<WideTail<D, NT>*>(smem + 2 * S::kStages * S::kSide);
+  WideTail<D, NT>& T = *reinterpret_cast<WideTail<D, NT>*>(smem + (S::kKStages + S::kVStages) * S::kSide);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t k_ring = base, v_ring = base + S::kStages * S::kSide;
-  const uint32_t k_full = smem_u32(T.k_full), v_full = smem_u32(T.v_full), v_free = smem_u32(T.v_free),
+  const uint32_t k_ring = base, v_ring = base + S::kKStages * S::kSide;
+  const uint32_t k_full = smem_u32(T.k_full), k_free = smem_u32(T.k_free), v_full = smem_u32(T.v_full), v_free = smem_u32(T.v_free),
                  s_full = smem_u32(T.s_full), p_full = smem_u32(T.p_full), p_free = smem_u32(T.p_free);
   const uint64_t pol = l2_evict_first();
   if (warp == kSoftWarps + kMmaWarp) {
@@ -145,8 +149,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
+    for (int s = 0; s < S::kKStages; ++s) {
       mbar_init(k_full + 8 * s, kBoxes);
+      mbar_init(k_free + 8 * s, 1);
+    }
+    for (int s = 0; s < S::kVStages; ++s) {
       mbar_init(v_full + 8 * s, kBoxes);
       mbar_init(v_free + 8 * s, kValueWarps);
     }
@@ -180,8 +187,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
   auto wait_for = [&](uint32_t bars, uint32_t it, int n, bool freed) {
     const uint32_t use = it / n;
     if (freed && use == 0) return;   // nothing was there before
-    if (!dead && !mbar_wait_bounded(bars + 8 * (it % n), (freed ? use - 1 : use) & 1, kAttnPolls)) dead = true;
-    dead = __any_sync(0xffffffffu, dead);
+    const uint32_t bar = bars + 8 * (it % n), parity = (freed ? use - 1 : use) & 1;
+    if (dead || __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+    dead = __any_sync(0xffffffffu, !mbar_wait_bounded(bar, parity, kAttnPolls));
   };
   // Block and first token of box b of tile i of the segment; block -1: not there.
   auto look_up = [&](int i, int b, int& block, int& tok) {
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     tok = 0;
     const int t = (sg.first + i) * kWideTile + b * kBox;
     if (i < sg.last - sg.first && t < sg.rq.kv) {
-      const int q = t / p.B;
+      const int q = block_index(p, t);
       const int id = p.table[(size_t)sg.r * p.max_blocks + q];
       tok = t - q * p.B;
       block = id >= 0 && id < p.n_blocks ? id : -1;
@@ -269,20 +277,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
       mbar_arrive(bar);
     }
   };
-  // The keys' copies: lanes 0 and 1 of a quad's first warp; the values': lanes 0-7 of a value warp.
-  const bool keys = warp < kQuads && lane < 2, values = warp == kSoftWarps + kCopyWarp && lane < kBoxes;
-  const int my_box = keys ? 2 * warp + lane : lane;
+  // Each value warp copies a box: lane 0 its keys, lane 1 its values. (A copy
+  // takes about 90 cycles to issue: all sixteen boxes' 32 panels from one warp
+  // took 2900 of a tile's 5800 cycles.)
+  const bool keys = lane == 0, copies = warp >= kSoftWarps && lane < 2;
+  const int my_box = warp - kSoftWarps;
+  const uint32_t my_bars = keys ? k_full : v_full, my_ring = keys ? k_ring : v_ring, my_stages = keys ? S::kKStages : S::kVStages;
   auto open_copies = [&]() {
-    const int ahead = min(T.seg[turn].last - T.seg[turn].first, S::kStages);
-    if (!dead && (keys || values)) {
-      int block[S::kStages], tok[S::kStages];
+    constexpr int kMost = S::kKStages > S::kVStages ? S::kKStages : S::kVStages;
+    const int ahead = min(T.seg[turn].last - T.seg[turn].first, (int)my_stages);
+    if (!dead && copies) {
+      int block[kMost], tok[kMost];
 #pragma unroll
-      for (int i = 0; i < S::kStages; ++i) look_up(i, my_box, block[i], tok[i]);
+      for (int i = 0; i < kMost; ++i) look_up(i, my_box, block[i], tok[i]);
 #pragma unroll
-      for (int i = 0; i < S::kStages; ++i)
+      for (int i = 0; i < kMost; ++i)
         if (i < ahead)
-          copy_box(keys ? k_full : v_full, keys ? k_ring : v_ring, keys ? &p.k : &p.v,
-                   (int)((phase_base + i) % S::kStages), my_box, block[i], tok[i]);
+          copy_box(my_bars, my_ring, keys ? &p.k : &p.v, (int)((phase_base + i) % my_stages), my_box, block[i], tok[i]);
     }
     __syncwarp();
   };
@@ -309,12 +320,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
       float l[kHalf];    // this thread's tokens' sums
 #pragma unroll
       for (int n = 0; n < kHalf; ++n) l[n] = 0.0f;
-      int k_block = -1, k_tok = 0;   // of the next keys to copy
-      if (keys) look_up(S::kStages, my_box, k_block, k_tok);
-      // the scales of this thread's box, asked for a tile ahead
-      auto scales_of = [&](int i, float& ks, float& vs) {
+      // This thread's box: its block is asked for two tiles ahead, its scales one.
+      auto block_of = [&](int i) {
         int b, tok;
         look_up(i, token / kBox, b, tok);
+        return b;
+      };
+      auto scales_of = [&](int b, float& ks, float& vs) {
         ks = -1.0f;   // the block is not there
         vs = 1.0f;
         if (b >= 0) {
@@ -324,12 +336,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
         }
       };
       float ks_n, vs_n;
-      scales_of(0, ks_n, vs_n);
+      int block_n = block_of(1);
+      scales_of(block_of(0), ks_n, vs_n);
       for (int i = 0; i < tiles; ++i) {
         const uint32_t it = phase_base + i;
         const int buf = (int)(it & 1);
         const float ks = ks_n, vs = fminf(fmaxf(vs_n, 0x1p-60f), 0x1p60f);
-        scales_of(i + 1, ks_n, vs_n);
+        scales_of(block_n, ks_n, vs_n);
+        block_n = block_of(i + 2);
         const float lvs = log2f(vs), rvs = 1.0f / vs;
         const int tok = (cur.first + i) * kWideTile + token, own = tok - seen0;
         const bool there = ks != -1.0f && tok < rq.kv;
@@ -338,26 +352,22 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
         const int hidden = !there ? S::kRows : own > 0 ? min(max(own * p.G - cur.row0, 0), S::kRows) : 0;
         const bool ragged = __any_sync(0xffffffffu, !there || own > 0);
         wait_for(s_full, it, 2, false);
-        if (keys && !dead && i + S::kStages < tiles)   // the products have read the keys
-          copy_box(k_full, k_ring, &p.k, (int)(it % S::kStages), my_box, k_block, k_tok);
-        if (keys) look_up(i + S::kStages + 1, my_box, k_block, k_tok);
-        __syncwarp();
         fence_after();
         const uint32_t s_at = tmem + buf * 128 + ((uint32_t)(32 * quad) << 16) + row_a;
         const float2* const rows = T.row + row_a;
         // exponents of every row, less the running maximum
         float x[kHalf];
         float top = -INFINITY;
+        uint32_t hi[kHalf], lo[kHalf];
 #pragma unroll
-        for (int n = 0; n < kHalf; n += 8) {
-          uint32_t hi[8], lo[8];
-          load_scores(s_at + n, s_at + S::kRows + n, hi, lo);
-          wait_scores(hi, lo);
+        for (int n = 0; n < kHalf; n += 8) load_scores(s_at + n, s_at + S::kRows + n, hi + n, lo + n);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float2 row = rows[n + k];
-            x[n + k] = fmaf(fmaf(__uint_as_float(lo[k]), kLoScale, __uint_as_float(hi[k])), ks * row.x, lvs - row.y);
-          }
+        for (int n = 0; n < kHalf; n += 8) wait_scores(hi + n, lo + n);
+#pragma unroll
+        for (int n = 0; n < kHalf; n += 2) {
+          const float4 row = *reinterpret_cast<const float4*>(rows + n);
+          x[n] = fmaf(fmaf(__uint_as_float(lo[n]), kLoScale, __uint_as_float(hi[n])), ks * row.x, lvs - row.y);
+          x[n + 1] = fmaf(fmaf(__uint_as_float(lo[n + 1]), kLoScale, __uint_as_float(hi[n + 1])), ks * row.z, lvs - row.w);
         }
         fence_before();
         if (ragged) {
@@ -421,8 +431,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
           // a block, are zeroed (the memory may hold anything), and a NaN among
           // the rows' own tokens is taken out here and put back at the end for
           // the rows that do see it; 0 * NaN would reach the others.
-          wait_for(v_full, it, S::kStages, false);
-          const uint32_t side = v_ring + (uint32_t)(it % S::kStages) * S::kSide;
+          wait_for(v_full, it, S::kVStages, false);
+          const uint32_t side = v_ring + (uint32_t)(it % S::kVStages) * S::kSide;
           // the quad's two warps take its tokens in turn, a word a lane
           unsigned todo = __ballot_sync(0xffffffffu, !there || own > 0);
           const unsigned live = __ballot_sync(0xffffffffu, there);
@@ -471,26 +481,43 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
           for (int k = 0; k < 4; ++k) o[c][n][k] = 0.0f;
       auto score = [&](int i) {   // the whole warp: tile i's scores into their buffer, which is free
         const uint32_t it = phase_base + i;
-        wait_for(k_full, it, S::kStages, false);
+        wait_for(k_full, it, S::kKStages, false);
         if (!dead && lane == 0) {
           fence_after();
-          const uint32_t d = tmem + (it & 1) * 128, keys_at = k_ring + (it % S::kStages) * S::kSide;
+          const uint32_t d = tmem + (it & 1) * 128, keys_at = k_ring + (it % S::kKStages) * S::kSide;
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
             mma_scores(d, operand(keys_at + (k >> 2) * S::kPanel + (k & 3) * 32),
                        operand(smem_u32(T.q[k >> 2]) + (k & 3) * 32), S::kIdesc, k > 0);
+          commit(k_free + 8 * (it % S::kKStages));
           commit(s_full + 8 * (it & 1));
         }
         __syncwarp();
       };
       if (vw == kMmaWarp)
         for (int i = 0; i < min(tiles, 2); ++i) score(i);
+      // Copies go out while the tile's weights are awaited: keys a ring on, whose
+      // place the tile's scores have read, and values a stage less, whose
+      // place the value warps have left by then.
+      const int reach = keys ? S::kKStages : S::kVStages - 1;
+      int next_block = -1, next_tok = 0;   // of this lane's next box to copy
+      if (copies) look_up(keys ? reach : reach + 1, my_box, next_block, next_tok);
       for (int i = 0; i < tiles; ++i) {
         const uint32_t it = phase_base + i;
-        const int s = (int)(it % S::kStages), buf = (int)(it & 1);
+        const int s = (int)(it % S::kVStages), buf = (int)(it & 1);
+        {
+          // (not s_full, which the tile after next may have gone through by now)
+          wait_for(k_free, it + S::kKStages, S::kKStages, true);
+          if (i > 0) wait_for(v_free, it + S::kVStages - 1, S::kVStages, true);
+          if (copies && !dead && i + reach < tiles && (keys || i > 0)) {
+            copy_box(my_bars, my_ring, keys ? &p.k : &p.v, (int)((it + reach) % my_stages), my_box, next_block, next_tok);
+          }
+          __syncwarp();
+          if (copies && (keys || i > 0)) look_up(i + reach + 1, my_box, next_block, next_tok);
+        }
         wait_for(p_full, it, 2, false);
         if (vw == kMmaWarp && i + 2 < tiles) score(i + 2);   // P is there: its scores are read
-        wait_for(v_full, it, S::kStages, false);
+        wait_for(v_full, it, S::kVStages, false);
         if (T.moved[buf] != 0u) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -541,21 +568,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
           mbar_arrive(v_free + 8 * s);
           mbar_arrive(p_free + 8 * buf);
         }
-        if (vw == kCopyWarp && i + S::kStages < tiles) {
-          int block, tok;
-          look_up(i + S::kStages, my_box, block, tok);
-          wait_for(v_free, it + S::kStages, S::kStages, true);
-          if (values && !dead) copy_box(v_full, v_ring, &p.v, s, my_box, block, tok);
-          __syncwarp();
-        }
       }
     }
     if (dead && lane == 0) {
       T.failed = 1;
-      for (int s = 0; s < S::kStages; ++s) {   // the copies still on their way
-        mbar_wait_bounded(k_full + 8 * s, (int)((phase_base / S::kStages) & 1), kAttnPolls);
-        mbar_wait_bounded(v_full + 8 * s, (int)((phase_base / S::kStages) & 1), kAttnPolls);
-      }
+      // the copies still on their way
+      for (int s = 0; s < S::kKStages; ++s)
+        mbar_wait_bounded(k_full + 8 * s, (int)((phase_base / S::kKStages) & 1), kAttnPolls);
+      for (int s = 0; s < S::kVStages; ++s)
+        mbar_wait_bounded(v_full + 8 * s, (int)((phase_base / S::kVStages) & 1), kAttnPolls);
     }
     phase_base += tiles;
     if (tid == 0) T.more = T.walk.next(p, S::kRows, T.seg[turn ^ 1]);
