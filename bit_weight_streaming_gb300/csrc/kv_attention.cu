@@ -734,7 +734,7 @@ int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_str
   p.by_segment = (long long)n_requests * K * p.max_groups <= L.n_ctas;
   p.unit = L.form.wide ? kWideTile : kBox;
   p.least = L.form.wide ? 1 : kAttnWarps;   // a box for every warp
-  p.lead = 32 * kBox / p.unit;              // 512 tokens: swept over a factor of 16, LEAD_NOTE
+  p.lead = (L.form.wide ? 64 : 32) * kBox / p.unit;              // 512 tokens: swept over a factor of 16, LEAD_NOTE
   cudaStream_t st = as_stream(stream);
   cudaError_t e;
   if (D == 64) e = launch_attn_d<64>(L.form, p, st);

@@ -72,7 +72,7 @@ struct __align__(1024) WideTail {
   float factor[2][8 * NT];     // what O shrinks by before the tile, where moved is set
   uint32_t moved[2];
   uint32_t nan_mask[2][D];
-  unsigned long long k_full[Wide<D, NT>::kKStages], k_free[Wide<D, NT>::kKStages];
+  unsigned long long k_full[Wide<D, NT>::kKStages];
   unsigned long long v_full[Wide<D, NT>::kVStages], v_free[Wide<D, NT>::kVStages];
   unsigned long long s_full[2], p_full[2], p_free[2], drain;
   long long line_warp[kSoftWarps + kValueWarps];
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
   WideTail<D, NT>& T = *reinterpret_cast<WideTail<D, NT>*>(smem + (S::kKStages + S::kVStages) * S::kSide);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t k_ring = base, v_ring = base + S::kKStages * S::kSide;
-  const uint32_t k_full = smem_u32(T.k_full), k_free = smem_u32(T.k_free), v_full = smem_u32(T.v_full), v_free = smem_u32(T.v_free),
+  const uint32_t k_full = smem_u32(T.k_full), v_full = smem_u32(T.v_full), v_free = smem_u32(T.v_free),
                  s_full = smem_u32(T.s_full), p_full = smem_u32(T.p_full), p_free = smem_u32(T.p_free);
   const uint64_t pol = l2_evict_first();
   if (warp == kSoftWarps + kMmaWarp) {
@@ -149,10 +149,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
-    for (int s = 0; s < S::kKStages; ++s) {
-      mbar_init(k_full + 8 * s, kBoxes);
-      mbar_init(k_free + 8 * s, 1);
-    }
+    for (int s = 0; s < S::kKStages; ++s) mbar_init(k_full + 8 * s, kBoxes);
     for (int s = 0; s < S::kVStages; ++s) {
       mbar_init(v_full + 8 * s, kBoxes);
       mbar_init(v_free + 8 * s, kValueWarps);
@@ -277,11 +274,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
       mbar_arrive(bar);
     }
   };
-  // Each value warp copies a box: lane 0 its keys, lane 1 its values. (A copy
-  // takes about 90 cycles to issue: all sixteen boxes' 32 panels from one warp
-  // took 2900 of a tile's 5800 cycles.)
-  const bool keys = lane == 0, copies = warp >= kSoftWarps && lane < 2;
-  const int my_box = warp - kSoftWarps;
+  // Each warp copies a box, its first lane: warps 0-7 the keys', the value warps
+  // the values'. (A copy takes about 90 cycles to issue: all sixteen boxes' 32
+  // panels from one warp took 2900 of a tile's 5800 cycles.)
+  const bool keys = warp < kSoftWarps, copies = lane == 0;
+  const int my_box = warp & (kBoxes - 1);
   const uint32_t my_bars = keys ? k_full : v_full, my_ring = keys ? k_ring : v_ring, my_stages = keys ? S::kKStages : S::kVStages;
   auto open_copies = [&]() {
     constexpr int kMost = S::kKStages > S::kVStages ? S::kKStages : S::kVStages;
@@ -335,6 +332,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
           vs = p.v_scale[at];
         }
       };
+      int next_block = -1, next_tok = 0;   // of the next keys to copy
+      if (copies) look_up(S::kKStages, my_box, next_block, next_tok);
       float ks_n, vs_n;
       int block_n = block_of(1);
       scales_of(block_of(0), ks_n, vs_n);
@@ -460,7 +459,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
           proxy_fence();   // before TMA writes the stage again
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * buf);
+        if (lane == 0) {
+          mbar_arrive(p_full + 8 * buf);
+          // the tile's products have read its keys: the next into their place
+          if (!dead && i + S::kKStages < tiles)
+            copy_box(k_full, k_ring, &p.k, (int)(it % S::kKStages), my_box, next_block, next_tok);
+          look_up(i + S::kKStages + 1, my_box, next_block, next_tok);
+        }
+        __syncwarp();
       }
 #pragma unroll
       for (int n = 0; n < kHalf; ++n) {
@@ -489,31 +495,27 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
           for (int k = 0; k < D / 32; ++k)
             mma_scores(d, operand(keys_at + (k >> 2) * S::kPanel + (k & 3) * 32),
                        operand(smem_u32(T.q[k >> 2]) + (k & 3) * 32), S::kIdesc, k > 0);
-          commit(k_free + 8 * (it % S::kKStages));
           commit(s_full + 8 * (it & 1));
         }
         __syncwarp();
       };
       if (vw == kMmaWarp)
         for (int i = 0; i < min(tiles, 2); ++i) score(i);
-      // Copies go out while the tile's weights are awaited: keys a ring on, whose
-      // place the tile's scores have read, and values a stage less, whose
-      // place the value warps have left by then.
-      const int reach = keys ? S::kKStages : S::kVStages - 1;
-      int next_block = -1, next_tok = 0;   // of this lane's next box to copy
-      if (copies) look_up(keys ? reach : reach + 1, my_box, next_block, next_tok);
+      // Values are copied while the tile's weights are awaited, a stage less than
+      // the ring: the value warps have left that place by then.
+      int next_block = -1, next_tok = 0;   // of the next box to copy
+      if (copies) look_up(S::kVStages, my_box, next_block, next_tok);
       for (int i = 0; i < tiles; ++i) {
         const uint32_t it = phase_base + i;
         const int s = (int)(it % S::kVStages), buf = (int)(it & 1);
-        {
-          // (not s_full, which the tile after next may have gone through by now)
-          wait_for(k_free, it + S::kKStages, S::kKStages, true);
-          if (i > 0) wait_for(v_free, it + S::kVStages - 1, S::kVStages, true);
-          if (copies && !dead && i + reach < tiles && (keys || i > 0)) {
-            copy_box(my_bars, my_ring, keys ? &p.k : &p.v, (int)((it + reach) % my_stages), my_box, next_block, next_tok);
+        if (i > 0) {
+          wait_for(v_free, it + S::kVStages - 1, S::kVStages, true);
+          if (copies) {
+            if (!dead && i + S::kVStages - 1 < tiles)
+              copy_box(v_full, v_ring, &p.v, (int)((it + S::kVStages - 1) % S::kVStages), my_box, next_block, next_tok);
+            look_up(i + S::kVStages, my_box, next_block, next_tok);
           }
           __syncwarp();
-          if (copies && (keys || i > 0)) look_up(i + reach + 1, my_box, next_block, next_tok);
         }
         wait_for(p_full, it, 2, false);
         if (vw == kMmaWarp && i + 2 < tiles) score(i + 2);   // P is there: its scores are read
