@@ -473,6 +473,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_
       const int step = solo ? Hd::kRows : kStep, mine = (solo ? 0 : warp * Hd::kRows) + sub;
       float* const stage = s_stage + (solo ? warp * p.solo_rows * D : 0) + sl * 8;
       const int staged = solo ? p.solo_rows : p.stage_rows;
+      if (!solo) __syncthreads();   // a warp may still read a short run's values where this one's will lie
       const float old = *scale_at;
       float amax = 0.0f;
       uint4 raw = row_at(row + mine);

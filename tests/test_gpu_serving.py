@@ -203,6 +203,25 @@ def test_append_long_runs(m):
                  freqs(64), None, None)
 
 
+@pytest.mark.parametrize("D,K,B,longest,R", [(128, 8, 16, 5, 48), (128, 8, 16, 16, 40), (64, 4, 32, 12, 60),
+                                             (256, 4, 16, 3, 50), (256, 2, 64, 20, 64), (64, 16, 16, 9, 400)])
+def test_append_short_and_long_runs_side_by_side(m, D, K, B, longest, R):
+    """Spans that hold runs of one warp's and of the whole CTA's, next to each other."""
+    for seed in range(3):
+        rng = np.random.RandomState(seed)
+        lens = [longest] + rng.randint(1, longest + 1, R - 1).tolist()
+        seqs = rng.randint(0, 3 * B, R)
+        table, n_blocks = tables([s + n for s, n in zip(seqs, lens)], B, seed=seed)
+        slots = [int(table[r, p // B]) * B + p % B for r in range(R) for p in range(seqs[r], seqs[r] + lens[r])]
+        pos = [p for r in range(R) for p in range(seqs[r], seqs[r] + lens[r])]
+        g = gen(seed)
+        cache = make_cache(m, n_blocks, K, B, D)
+        fill(cache, g)
+        n, w = len(pos), torch.ones(D, device=device())
+        check_append(m, cache, held(cache), rows(n, 2, D, g, 3.0), rows(n, K, D, g, 3.0), rows(n, K, D, g, 3.0), pos, slots,
+                     freqs(D), w, w)
+
+
 def test_append_special_values(m):
     """Zero rows, infinities and NaN: they set no scale, NaN stays, infinity saturates."""
     D, K, B = 64, 1, 16
