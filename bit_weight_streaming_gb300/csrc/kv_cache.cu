@@ -226,6 +226,23 @@ BWS_DEV void norm_head(float (&x)[8], const float (&w)[8], float eps) {
 // and SM here (formed that way, f alone held the FP64 pipe 73 % busy in a
 // verify batch); only positions from 2^24 on take their product in it. Either
 // way the fraction is off by a few 2^-24.
+// sin and cos of 2 pi t, |t| <= 1/2: quarter turns off, then the Taylor series
+// within an eighth of a turn (terms to x^9 and x^8: 2^-25 and below is left out),
+// so that a key's rounding to E4M3 is its own and not the angle's. Half the
+// instructions of sincospif; the fast pair (2^-21) moved ten times the codes
+// across a midpoint.
+BWS_DEV void sincos_turn(float t, float& s, float& c) {
+  const float q = rintf(4.0f * t);
+  const float x = (t - 0.25f * q) * 6.2831853071795865f, z = x * x;   // t - q / 4 is exact
+  const float sx = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 2.7557319e-6f, -1.9841270e-4f), 8.3333333e-3f), -1.6666667e-1f), x);
+  const float cx = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 2.4801587e-5f, -1.3888889e-3f), 4.1666667e-2f), -0.5f), 1.0f);
+  const int n = (int)q;
+  s = (n & 1) ? cx : sx;
+  c = (n & 1) ? sx : cx;
+  if (n & 2) s = -s;
+  if ((n + 1) & 2) c = -c;
+}
+
 // The turn of a far position: FP64, out of line so that nothing of it runs for near ones.
 __device__ __noinline__ float far_turn(float f, int pos) {
   const double d = (double)f * 0.15915494309189533577 * (double)pos;
@@ -263,11 +280,8 @@ struct Angles {
       } else {
         t = far_turn(inv_freq[i], pos);
       }
-      // Within half a turn the fast pair is off by at most 2^-21, far below
-      // the 2^-9 and 2^-4 that the results are rounded by; sincospif's forty
-      // instructions a pair were a third of a key row's work.
       float s, c;
-      __sincosf(t * 6.2831853071795865f, &s, &c);
+      sincos_turn(t, s, c);
       cs[i] = make_float2(c, s);
     }
   }
