@@ -19,8 +19,10 @@ namespace {
 // of the rows and of the taken blocks, so one launch suffices and no CTA waits
 // for another. A row inside a block that this call takes reads it from the
 // free list, not from the table entry another CTA is writing.
-// Bound: launch and the chain of two dependent loads for few requests, the 8
-// bytes written per row for many.
+// Bound: launch and the chain of two dependent loads for few requests (one of
+// eight rows: 3.5 us); 384 requests with 374000 rows, 3.0 MB: 6.6 us, of which the
+// launch, the CTAs' own sums and the search of a row's request are all but half a
+// microsecond.
 
 constexpr int kPlanThreads = 256;
 constexpr int kPlanMaxRequests = 4096;
@@ -353,9 +355,12 @@ BWS_DEV void store_codes(uint8_t* p, const float (&x)[8], float inv) {
 // passes the values wait in shared memory (of a run that is longer than it, the
 // rest is formed again: the rows are in L1 by then). One rolled loop serves
 // short and long runs: with the short ones unrolled in registers a quarter of
-// the issue slots waited for instructions (a 12382-row chunk: 128 us).
-// Bound: launch and three dependent loads for a decoded token, the bytes of
-// the rows for a prompt chunk.
+// the issue slots waited for instructions (a 12382-row chunk: 128 us, and 162
+// with a CTA per run).
+// Bound: launch and three dependent loads for a decoded token (one: 3.8 us; 48
+// requests of five rows: 10.7 us, a serial run per warp). A 12382-row chunk at 64:
+// 55 us for 127 MB, 2.3 TB/s, by instructions: 54 % of the issue slots, the
+// conversions, norms and rotations of 38 million values.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_constant__ AppendParams p) {
   using Hd = Head<D>;
