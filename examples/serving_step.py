@@ -50,7 +50,6 @@ class Model:
         x = x + bws.nvfp4_gemv(*self.out, a.view(-1, Q_HEADS * DIM), ws=self.ws)
         return torch.softmax(bws.fp8_lmhead_gemv(*self.head, x, ws=self.ws), -1)
 
-
     def draft(self, token, n):
         """n tokens drawn one after the other from the output layer on the embedding, and their probabilities."""
         tokens, probs = [], []
