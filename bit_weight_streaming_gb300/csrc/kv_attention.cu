@@ -51,12 +51,15 @@ struct Shape {
   static constexpr int kSide = kBox * D;                     // bytes of a unit's keys, or values
   static constexpr int kStage = 2 * kSide;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kJoin = kRows * D * 4;                 // a warp's O in FP32, for the segment's end
+  // a warp's O in FP32, for the segment's end; four words between rows put the
+  // eight rows of a store on all banks
+  static constexpr int kJoinRow = D + 4;
+  static constexpr int kJoin = kRows * kJoinRow * 4;
   // Up to NT * D = 256 the warps' O has memory of its own, so that the next
   // segment's copies run during the join; wider ones use the drained ring.
   static constexpr bool kOverlap = NT * D <= 256;
   static constexpr int kCtas = NT * D <= 128 ? 2 : 1;         // CTAs an SM, by registers
-  static constexpr int kStages = !kOverlap ? NT + (D == 256) : ((kCtas == 2 ? 96 : 192) * 1024 / kAttnWarps - kJoin) / kStage;
+  static constexpr int kStages = !kOverlap ? NT + 1 : ((kCtas == 2 ? 100 : 200) * 1024 / kAttnWarps - kJoin) / kStage;
   static constexpr int kRing = kStages * kStage;
   static constexpr int kWarpBytes = kRing + (kOverlap ? kJoin : 0);
   static constexpr bool kQInRegs = NT * D <= 256;
@@ -137,26 +140,33 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
       }
     }
   };
-  // Scales of 32 units, one a lane: ks (-1: the block is not there), log2(vs), 1 / vs.
+  // Scales of 32 units, one a lane: ks (-1: the block is not there) and vs as
+  // they are read, and when they are used log2(vs) and 1 / vs.
   struct Scales {
-    float ks, lvs, rvs;
+    float ks, vs;
   };
-  Scales sc_l, sc_n;
+  Scales sc_n;
+  float ks_l, lvs_l, rvs_l;
   auto scales_of = [&](int b) {
-    Scales s = {-1.0f, 0.0f, 0.0f};
+    Scales s = {-1.0f, 1.0f};
     if (b >= 0) {
       const size_t at = (size_t)b * p.K + sg.head;
       s.ks = p.k_scale[at];
-      const float vs = fminf(fmaxf(p.v_scale[at], 0x1p-60f), 0x1p60f);
-      s.lvs = log2f(vs);
-      s.rvs = 1.0f / vs;
+      s.vs = p.v_scale[at];
     }
     return s;
   };
-  // A segment's start: its first copies, scales and this warp's query rows are
-  // asked for together; nothing here waits but the copies for the block ids.
-  uint16_t qx[NT][D / 32];
-  auto open_segment = [&]() {
+  auto use_scales = [&](const Scales& s) {
+    const float vs = fminf(fmaxf(s.vs, 0x1p-60f), 0x1p60f);
+    ks_l = s.ks;
+    lvs_l = log2f(vs);
+    rvs_l = 1.0f / vs;
+  };
+  // A segment's start, in two steps, so that block ids and query rows are on
+  // their way while the segment before is joined: what is asked for first, and
+  // the copies and scales that need the ids.
+  uint32_t qx[NT][D / 64];   // dimensions 2 lane + 64 i and the next, BF16
+  auto ask_segment = [&]() {
     mine = (sg.last - sg.first - warp + kAttnWarps - 1) / kAttnWarps;
     look_up(lane, ids, toks);
     const int n_rows = min(sg.rq.rows * p.G - sg.row0, S::kRows);
@@ -165,38 +175,40 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
       const int n = warp + k * kAttnWarps;
       if (n < n_rows) {
         const int j = (sg.row0 + n) / p.G, h = sg.head * p.G + (sg.row0 + n) % p.G;
-        const uint16_t* src = p.q + (sg.rq.start + j) * p.q_row_stride + h * p.q_head_stride + lane;
+        const uint16_t* src = p.q + (sg.rq.start + j) * p.q_row_stride + h * p.q_head_stride + 2 * lane;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) qx[k][i] = src[32 * i];
+        for (int i = 0; i < D / 64; ++i) qx[k][i] = *reinterpret_cast<const uint32_t*>(src + 64 * i);
       } else {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) qx[k][i] = 0;
+        for (int i = 0; i < D / 64; ++i) qx[k][i] = 0;
       }
     }
+  };
+  auto open_segment = [&]() {
     if (!dead) {
       const int ahead = min(mine, S::kStages);
       for (int i = 0; i < ahead; ++i) issue(i, (int)((phase_base + i) % S::kStages));
     }
-    sc_l = scales_of(ids);
+    sc_n = scales_of(ids);
   };
   // The query rows to f16, each scaled by a power of two. `slot`: the NaN mask to clear.
   auto store_queries = [&](int slot) {
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
       const int n = warp + k * kAttnWarps;
-      uint16_t* dst = reinterpret_cast<uint16_t*>(T.q + n * S::kQStride);
+      __half2* dst = reinterpret_cast<__half2*>(T.q + n * S::kQStride);
       float x[D / 32];
       float top = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        x[i] = __uint_as_float((uint32_t)qx[k][i] << 16);
+        x[i] = __uint_as_float(i % 2 ? qx[k][i / 2] & 0xFFFF0000u : qx[k][i / 2] << 16);
         if (fabsf(x[i]) < INFINITY) top = fmaxf(top, fabsf(x[i]));
       }
       top = warp_max(top);
       const int e = top > 0.0f ? min(max(floor_log2_abs(top), -100), 126) : 0;
       const float f = exp2i(-e);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = __half_as_ushort(__float2half_rn(x[i] * f));
+      for (int i = 0; i < D / 64; ++i) dst[lane + 32 * i] = __floats2half2_rn(x[2 * i] * f, x[2 * i + 1] * f);
       if (lane == 0) T.q_scale[n] = p.scale * kLog2e * exp2i(e);
     }
     for (int i = tid; i < D; i += kAttnThreads) T.nan_mask[slot][i] = 0;
@@ -205,6 +217,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
   bool more = walk.next(p, S::kRows, sg);
   int turn = 0;
   if (more) {
+    ask_segment();
     open_segment();
     store_queries(0);
   }
@@ -246,6 +259,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[c][n][k] = 0.0f;
 
+    use_scales(sc_n);
     for (int i = 0; i < mine; ++i) {
       const uint32_t it = phase_base + i;
       const int s = (int)(it % S::kStages);
@@ -265,11 +279,11 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
         look_up((i & ~31) + 32 + lane, b, tok);
         sc_n = scales_of(b);
       }
-      if ((i & 31) == 0 && i > 0) sc_l = sc_n;
-      const float ks = __shfl_sync(0xffffffffu, sc_l.ks, i & 31);
+      if ((i & 31) == 0 && i > 0) use_scales(sc_n);
+      const float ks = __shfl_sync(0xffffffffu, ks_l, i & 31);
       const int tok0 = token_of(i);
       if (ks != -1.0f) {
-        const float lvs = __shfl_sync(0xffffffffu, sc_l.lvs, i & 31), rvs = __shfl_sync(0xffffffffu, sc_l.rvs, i & 31);
+        const float lvs = __shfl_sync(0xffffffffu, lvs_l, i & 31), rvs = __shfl_sync(0xffffffffu, rvs_l, i & 31);
         // ---- S^T: 16 tokens x rows
         // (two chains of sums, of even and of odd chunks, where the rows are few)
         constexpr int kChains = NT == 1 ? 2 : 1;
@@ -411,7 +425,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
 
     // ---- the segment's end: join the warps' m, l, O
     more = walk.next(p, S::kRows, sg);
-    if (S::kOverlap && more) open_segment();
+    if (more) ask_segment();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -431,9 +445,10 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float2*>(own + (n * 8 + t4 * 2 + k) * D + c * 16 + 2 * g) =
+            *reinterpret_cast<float2*>(own + (n * 8 + t4 * 2 + k) * S::kJoinRow + c * 16 + 2 * g) =
                 make_float2(o[c][n][k], o[c][n][k + 2]);
     }
+    if (S::kOverlap && more) open_segment();
     __syncthreads();
     const bool whole = cur.whole;
     const int slot = cta * 2 + (cur.starts ? 1 : 0);
@@ -447,7 +462,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
       for (int w = 0; w < n_live; ++w) {
         const float mw = T.m[w][n];
         const float f = exp2_fast(mw - top);
-        const float4 b = *reinterpret_cast<const float4*>(join + w * kJoinStep + n * D + d);
+        const float4 b = *reinterpret_cast<const float4*>(join + w * kJoinStep + n * S::kJoinRow + d);
         sum = fmaf(T.l[w][n], f, sum);
         a.x = fmaf(b.x, f, a.x);
         a.y = fmaf(b.y, f, a.y);
