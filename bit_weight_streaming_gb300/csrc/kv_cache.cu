@@ -251,87 +251,153 @@ __device__ __noinline__ float far_turn(float f, int pos) {
   return (float)(d - rint(d));
 }
 
+// How a head's pairs lie: (2 i, 2 i + 1); (i, i + half) with half a whole number
+// of lanes' eights; any other half.
+enum Pairs { kInterleaved, kSplitLanes, kSplitAny };
+
+// A lane forms four of a row's angles: of the pairs it holds (interleaved), or
+// half of the eight that it shares with the lane of the pairs' other halves, which
+// a shuffle brings. Only kSplitAny takes them through shared memory: as a table
+// there, read eight words apart by neighbouring lanes, they cost a round of keys
+// 2500 cycles (a 628-row chunk at 256: 50 us, now 31). Where at most half of the
+// head turns, the group's upper lanes form two of the lower lanes' four.
 template <int D>
 struct Angles {
-  static constexpr int kEach = D / 2 / Head<D>::kLanes;   // pairs a lane forms: sl + k * kLanes
-  float fh[kEach], fl[kEach];
+  float fh[4], fl[4];
 
-  BWS_DEV void init(const float* inv_freq, int half, int sl) {
+  static BWS_DEV bool helped(Pairs pairs, int half) { return pairs != kSplitAny && 4 * half <= D; }
+  static BWS_DEV int pair_of(Pairs pairs, int k, int half, int sl) {
+    if (helped(pairs, half) && sl >= Head<D>::kLanes / 2) {
+      sl -= Head<D>::kLanes / 2;
+      k += 2;
+    }
+    const int base = sl * 8;
+    if (pairs == kInterleaved) return sl * 4 + k;
+    if (pairs == kSplitLanes) return base < half ? base + k : base - half + 4 + k;
+    return sl + k * Head<D>::kLanes;
+  }
+  BWS_DEV void init(const float* inv_freq, Pairs pairs, int half, int sl) {
     constexpr double kTurn = 0.15915494309189533577;      // 1 / 2 pi
     constexpr float kHi = (float)kTurn, kLo = (float)(kTurn - (double)kHi);
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int i = sl + k * Head<D>::kLanes;
+    for (int k = 0; k < 4; ++k) {
+      const int i = pair_of(pairs, k, half, sl);
       const float f = i < half ? inv_freq[i] : 0.0f;
       fh[k] = f * kHi;
       fl[k] = fmaf(f, kLo, fmaf(f, kHi, -fh[k]));
     }
   }
-  BWS_DEV void form(int pos, const float* inv_freq, int half, int sl, float2* cs) const {
-    const float fp = (float)pos;
-    const bool near = pos < (1 << 24) && pos > -(1 << 24);
+  // c, s: of this lane's eight values, s with the sign that its partner's value
+  // takes (interleaved: of its four pairs). cs: the group's table for kSplitAny.
+  BWS_DEV void form(int pos, const float* inv_freq, Pairs pairs, int half, int sl, float2* cs, float (&c)[8],
+                    float (&s)[8]) const {
+    const int base = sl * 8;
+    const bool help = helped(pairs, half);   // k = 2, 3 come from other lanes
+    float t[4], u[4], v[4];
+    if (pos < (1 << 24) && pos > -(1 << 24)) {
+      const float fp = (float)pos;
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int i = sl + k * Head<D>::kLanes;
-      if (i >= half) break;
-      float t;
-      if (near) {
+      for (int k = 0; k < 4; ++k) {
+        if (k >= 2 && help) break;
         const float a = fh[k] * fp, e = fmaf(fh[k], fp, -a);
-        t = (a - rintf(a)) + fmaf(fl[k], fp, e);
-        t -= rintf(t);
-      } else {
-        t = far_turn(inv_freq[i], pos);
+        t[k] = (a - rintf(a)) + fmaf(fl[k], fp, e);
+        t[k] -= rintf(t[k]);
       }
-      float s, c;
-      sincos_turn(t, s, c);
-      cs[i] = make_float2(c, s);
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const int i = pair_of(pairs, k, half, sl);
+        const float x = i < half ? far_turn(inv_freq[i], pos) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[j] = j == k ? x : t[j];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= 2 && help) break;
+      sincos_turn(t[k], v[k], u[k]);
+    }
+    if (help) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        u[k + 2] = __shfl_down_sync(0xffffffffu, u[k], Head<D>::kLanes / 2);
+        v[k + 2] = __shfl_down_sync(0xffffffffu, v[k], Head<D>::kLanes / 2);
+      }
+    }
+    if (pairs == kInterleaved) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        c[k] = u[k];
+        s[k] = v[k];
+      }
+    } else if (pairs == kSplitLanes) {
+      const bool low = base < half;
+      const int partner = (threadIdx.x & 31) + (low ? half >> 3 : base < 2 * half ? -(half >> 3) : 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float pu = __shfl_sync(0xffffffffu, u[k], partner), pv = __shfl_sync(0xffffffffu, v[k], partner);
+        c[k] = low ? u[k] : pu;
+        s[k] = low ? -v[k] : pv;
+        c[k + 4] = low ? pu : u[k];
+        s[k + 4] = low ? -pv : v[k];
+      }
+    } else {
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = sl + k * Head<D>::kLanes;
+        if (i < half) cs[i] = make_float2(u[k], v[k]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int d = base + k;
+        const float2 a = d < 2 * half ? cs[d < half ? d : d - half] : make_float2(1.0f, 0.0f);
+        c[k] = a.x;
+        s[k] = d < half ? -a.y : a.y;
+      }
     }
   }
 };
 
-// Rotates a head; cs: its row's angles, buf: the group's own D floats (used
-// where a pair's halves do not lie a whole number of lanes apart).
+// Rotates a head by its row's angles; buf: the group's own D floats for kSplitAny.
 template <int D>
-BWS_DEV void rotate_head(float (&x)[8], const float2* cs, int rot, bool interleaved, float* buf, int sl) {
-  const int base = sl * 8, half = rot >> 1;
-  if (interleaved) {
+BWS_DEV void rotate_head(float (&x)[8], const float (&c)[8], const float (&s)[8], Pairs pairs, int half, float* buf,
+                         int sl) {
+  const int base = sl * 8, rot = 2 * half;
+  if (pairs == kInterleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      if (base + i < rot) {
-        const float2 a = cs[(base + i) >> 1];
-        const float u = x[i], v = x[i + 1];
-        x[i] = u * a.x - v * a.y;
-        x[i + 1] = v * a.x + u * a.y;
+    for (int k = 0; k < 4; ++k) {
+      if (base + 2 * k < rot) {
+        const float u = x[2 * k], v = x[2 * k + 1];
+        x[2 * k] = u * c[k] - v * s[k];
+        x[2 * k + 1] = v * c[k] + u * s[k];
       }
     }
     return;
   }
   float y[8];
-  if ((half & 7) == 0) {
-    const int step = half >> 3;
-    const int from = base < half ? step : base < rot ? -step : 0;
+  if (pairs == kSplitLanes) {
+    const int partner = (threadIdx.x & 31) + (base < half ? half >> 3 : base < rot ? -(half >> 3) : 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], (threadIdx.x & 31) + from);
-  } else {
-    __syncwarp();   // the last head's reads of buf are done
+    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], partner);
+    if (base < rot) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) buf[base + i] = x[i];
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int d = base + i;
-      y[i] = d < half ? buf[d + half] : d < rot ? buf[d - half] : 0.0f;
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + y[i] * s[i];
     }
+    return;
   }
+  __syncwarp();   // the last head's reads of buf are done
+#pragma unroll
+  for (int i = 0; i < 8; ++i) buf[base + i] = x[i];
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int d = base + i;
-    if (d < rot) {
-      const float2 a = cs[d < half ? d : d - half];
-      x[i] = x[i] * a.x + y[i] * (d < half ? -a.y : a.y);
-    }
+    if (d < rot) x[i] = x[i] * c[i] + buf[d < half ? d + half : d - half] * s[i];
   }
 }
+
 
 // e of the smallest 2^e with amax <= 448 * 2^e, in [-60, 60]; 448 = 1.75 * 2^8.
 BWS_DEV int scale_exponent(float amax) {
@@ -366,14 +432,16 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_
   using Hd = Head<D>;
   constexpr int kStep = kAppendWarps * Hd::kRows;   // rows of a key/value CTA's round
   extern __shared__ __align__(16) float s_stage[];  // [stage_rows][D]
-  __shared__ __align__(16) float2 s_cs[kAppendWarps][Hd::kRows][D / 2];
   __shared__ float s_amax[kAppendWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / Hd::kLanes, sl = lane % Hd::kLanes;
   const bws_qkv& in = p.in;
   const int half = in.rot >> 1;
-  float2* const cs = s_cs[warp][sub];
-  float* const buf = s_stage + p.stage_rows * D + (warp * Hd::kRows + sub) * D;   // there where a pair needs it
+  // a group's heads and angles, there where kSplitAny needs them
+  float* const buf = s_stage + (p.stage_rows + warp * Hd::kRows + sub) * D;
+  float2* const cs = reinterpret_cast<float2*>(s_stage + (p.stage_rows + (kAppendWarps + warp) * Hd::kRows + sub) * D);
+  const Pairs pairs = in.interleaved ? kInterleaved : half % 8 == 0 ? kSplitLanes : kSplitAny;
+  float cos_of[8], sin_of[8];
   pdl_launch_dependents();
   pdl_wait();
   Angles<D> angles;
@@ -394,9 +462,8 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_
     }
     if (half > 0) {
       const int pos = in.positions[live ? row : row0];
-      angles.init(in.inv_freq, half, sl);
-      angles.form(pos, in.inv_freq, half, sl, cs);
-      __syncwarp();
+      angles.init(in.inv_freq, pairs, half, sl);
+      angles.form(pos, in.inv_freq, pairs, half, sl, cs, cos_of, sin_of);
     }
     for (int h = h0; h < h1; ++h) {
       const uint4 now = raw;
@@ -404,7 +471,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_
       float x[8];
       unpack8(now, x);
       if (in.q_weight != nullptr) norm_head<D>(x, w, in.eps);
-      if (half > 0) rotate_head<D>(x, cs, in.rot, in.interleaved != 0, buf, sl);
+      if (half > 0) rotate_head<D>(x, cos_of, sin_of, pairs, half, buf, sl);
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -434,15 +501,13 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = in.k_weight[sl * 8 + i];
   }
-  if (turned) angles.init(in.inv_freq, half, sl);
+  if (turned) angles.init(in.inv_freq, pairs, half, sl);
   auto form = [&](const uint4& raw, int pos, float (&x)[8]) {
     unpack8(raw, x);
     if (normed) norm_head<D>(x, w, in.eps);
     if (turned) {
-      __syncwarp();
-      angles.form(pos, in.inv_freq, half, sl, cs);
-      __syncwarp();
-      rotate_head<D>(x, cs, in.rot, in.interleaved != 0, buf, sl);
+      angles.form(pos, in.inv_freq, pairs, half, sl, cs, cos_of, sin_of);
+      rotate_head<D>(x, cos_of, sin_of, pairs, half, buf, sl);
     }
   };
 
@@ -585,7 +650,7 @@ cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem, cud
 template <int D>
 cudaError_t launch_append(unsigned grid, size_t smem, cudaStream_t st, const AppendParams& p) {
   static std::atomic<unsigned long long> attr{0};
-  const cudaError_t e = set_smem_once(attr, append_kernel<D>, kAppendWarps * 9 * 256 * 4);
+  const cudaError_t e = set_smem_once(attr, append_kernel<D>, kAppendWarps * 10 * 256 * 4);
   return e != cudaSuccess ? e : launch_pdl(append_kernel<D>, grid, kAppendThreads, smem, st, p);
 }
 
@@ -712,7 +777,7 @@ int bws_qk_norm_rope_append(const bws_qkv* in, const bws_kv_cache* cache, uint16
   p.solo_rows = round * (rows * K * 2 >= sms * 16 ? 8 : 2);
   p.stage_rows = kAppendWarps * p.solo_rows;
   const bool pair_buffer = !in->interleaved && (in->rot / 2) % 8 != 0;
-  const size_t smem = (size_t)p.stage_rows * D * 4 + (pair_buffer ? kAppendWarps * 256 * 4 : 0);
+  const size_t smem = (size_t)p.stage_rows * D * 4 + (pair_buffer ? 2 * kAppendWarps * 256 * 4 : 0);
   const unsigned grid = (unsigned)(kv_ctas + q_ctas);
   cudaStream_t st = as_stream(stream);
   cudaError_t e;
