@@ -27,9 +27,9 @@
 // reads without bank conflicts) and keeps its own m, l and O in registers; no
 // barrier joins them before the segment's end.
 // Bound: for few rows HBM and what a CTA spends at its start, a segment's end and
-// the join. One request of 131071 tokens, four kv heads of 256, one row: 53 us
-// for 268 MB (5.0 TB/s; 8 us of it start, end and join). 80 requests, 751 MB at
-// 128: 124 us (6.1 TB/s). 24 requests of five rows at 64, 141 MB: 37 us (3.8
+// the join. One request of 131071 tokens, four kv heads of 256, one row: 52 us
+// for 268 MB (5.1 TB/s; 8 us of it start, end and join). 80 requests, 751 MB at
+// 128: 121 us (6.2 TB/s). 24 requests of five rows at 64, 141 MB: 36 us (3.9
 // TB/s), where half the cycles issue: a unit there is 2 KB against as many
 // instructions of softmax a token as at 256. Two CTAs an SM up to NT D = 128.
 // Copies of several boxes at once, and keys' and values' rings apart, lost 2 to

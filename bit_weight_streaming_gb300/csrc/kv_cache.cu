@@ -424,7 +424,7 @@ BWS_DEV void store_codes(uint8_t* p, const float (&x)[8], float inv) {
 // the issue slots waited for instructions (a 12382-row chunk: 128 us, and 162
 // with a CTA per run).
 // Bound: launch and three dependent loads for a decoded token (one: 3.8 us; 48
-// requests of five rows: 10.7 us, a serial run per warp). A 12382-row chunk at 64:
+// requests of five rows: 8.8 us, a serial run per warp). A 12382-row chunk at 64:
 // 55 us for 127 MB, 2.3 TB/s, by instructions: 54 % of the issue slots, the
 // conversions, norms and rotations of 38 million values.
 template <int D>
