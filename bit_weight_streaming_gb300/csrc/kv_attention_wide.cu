@@ -595,34 +595,63 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     } else {
       const int vw = warp - kSoftWarps, row0 = cur.row0, n_group_rows = min(rq.rows * p.G - row0, S::kRows);
       const int slot = blockIdx.x * 2 + (cur.starts ? 1 : 0);
+      const bool whole = cur.whole;
+      // A row's place, factor and sight are formed by a lane of their own and
+      // shuffled to those that hold the row: this code runs once a segment, and
+      // formed by each for its rows (divisions, sums, twelve times over) it was
+      // the fetching of its instructions that took 12000 cycles.
+      constexpr int kSets = (S::kRows + 31) / 32;
+      long long place[kSets];
+      float factor[kSets];
+      uint32_t see[kSets];
+#pragma unroll
+      for (int q = 0; q < kSets; ++q) {
+        const int row = q * 32 + lane, live = min(row, n_group_rows - 1);
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kQuads; ++w) sum += T.l[w][live];
+        const int j = (row0 + live) / p.G, h = cur.head * p.G + (row0 + live) - j * p.G;
+        const long long at = (long long)(rq.start + j) * p.H + h, part = (long long)slot * S::kRows + live;
+        place[q] = (whole ? at : part) * D;
+        factor[q] = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+        see[q] = (2u << j) - 1u;
+        if (vw == 0 && row < n_group_rows) {
+          if (!whole) p.part_ml[part] = make_float2(T.m[row], sum);
+          else if (p.lse != nullptr) p.lse[at] = sum == 0.0f ? -INFINITY : (T.m[row] + log2f(sum)) * kLn2;
+        }
+      }
+      constexpr int kOwn = S::kMT * 16;   // this warp's dimensions
+      if (__any_sync(0xffffffffu, lane < kOwn && nan_mask[vw * kOwn + (lane & (kOwn - 1))] != 0u)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t sight = __shfl_sync(0xffffffffu, see[n / 4], (n & 3) * 8 + t4 * 2 + k);
+#pragma unroll
+            for (int c = 0; c < S::kMT; ++c) {
+              const int d = vw * kOwn + c * 16 + 2 * g;
+              if (nan_mask[d] & sight) o[c][n][k] = NAN;
+              if (nan_mask[d + 1] & sight) o[c][n][k + 2] = NAN;
+            }
+          }
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int row = n * 8 + t4 * 2 + k;
-          if (row >= n_group_rows) continue;
-          float sum = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kQuads; ++w) sum += T.l[w][row];
-          const int j = (row0 + row) / p.G, h = cur.head * p.G + (row0 + row) % p.G;
-          const size_t at = (size_t)(rq.start + j) * p.H + h;
-          const uint32_t see = (2u << j) - 1u;
-          const float inv = cur.whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+          const int from = (n & 3) * 8 + t4 * 2 + k;
+          const long long at = __shfl_sync(0xffffffffu, place[n / 4], from) + vw * kOwn + 2 * g;
+          const float f = __shfl_sync(0xffffffffu, factor[n / 4], from);
+          if (n * 8 + t4 * 2 + k >= n_group_rows) continue;
 #pragma unroll
           for (int c = 0; c < S::kMT; ++c) {
-            const int d = (vw * S::kMT + c) * 16 + 2 * g;
-            const float a = (nan_mask[d] & see) ? NAN : o[c][n][k] * inv;
-            const float b = (nan_mask[d + 1] & see) ? NAN : o[c][n][k + 2] * inv;
-            if (cur.whole) {
+            const float a = o[c][n][k] * f, b = o[c][n][k + 2] * f;
+            if (whole) {
               const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-              *reinterpret_cast<uint32_t*>(p.out + at * D + d) = *reinterpret_cast<const uint32_t*>(&v);
+              *reinterpret_cast<uint32_t*>(p.out + at + c * 16) = *reinterpret_cast<const uint32_t*>(&v);
             } else {
-              *reinterpret_cast<float2*>(p.part_o + ((size_t)slot * S::kRows + row) * D + d) = make_float2(a, b);
+              *reinterpret_cast<float2*>(p.part_o + at + c * 16) = make_float2(a, b);
             }
-          }
-          if (vw == 0 && g == 0) {
-            if (!cur.whole) p.part_ml[(size_t)slot * S::kRows + row] = make_float2(T.m[row], sum);
-            else if (p.lse != nullptr) p.lse[at] = sum == 0.0f ? -INFINITY : (T.m[row] + log2f(sum)) * kLn2;
           }
         }
     }
