@@ -208,28 +208,33 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     constexpr int E = D / 32;   // neighbouring values a lane
     const Segment& sg = T.seg[turn];
     const int n_rows = min(sg.rq.rows * p.G - sg.row0, S::kRows);
-    uint2 raw[NT][E / 4];       // every row is asked for before the first is used
+    // Every row is asked for before the first is used; lane r knows where the r-th
+    // lies. The rows are then converted by one rolled loop, whose instructions
+    // are fetched once.
+    uint2 raw[NT][E / 4];
+    const int of_lane = min(warp + lane * kSoftWarps, max(n_rows - 1, 0));
+    const int of_j = (sg.row0 + of_lane) / p.G, of_h = sg.head * p.G + (sg.row0 + of_lane) - of_j * p.G;
+    const long long at_lane = (sg.rq.start + of_j) * p.q_row_stride + of_h * p.q_head_stride;
 #pragma unroll
     for (int r = 0; r < NT; ++r) {
-      const int n = warp + r * kSoftWarps;
-      const bool live = n < n_rows;
-      const int j = live ? (sg.row0 + n) / p.G : 0, h = sg.head * p.G + (live ? (sg.row0 + n) % p.G : 0);
-      const uint16_t* src = p.q + (sg.rq.start + j) * p.q_row_stride + h * p.q_head_stride + lane * E;
+      const uint16_t* src = p.q + __shfl_sync(0xffffffffu, at_lane, r) + lane * E;
+      const bool live = warp + r * kSoftWarps < n_rows;
 #pragma unroll
       for (int i = 0; i < E / 4; ++i) raw[r][i] = live ? *reinterpret_cast<const uint2*>(src + 4 * i) : make_uint2(0u, 0u);
     }
-#pragma unroll
-    for (int r = 0; r < NT; ++r) {
-      const int n = warp + r * kSoftWarps;
+#pragma unroll 1
+    for (int n = warp; n < S::kRows; n += kSoftWarps) {
       float x[E];
       float top = 0.0f;
       bool bad = false;   // an infinity would saturate: a row that holds one is all NaN, as its scores are
 #pragma unroll
       for (int i = 0; i < E / 4; ++i) {
-        x[4 * i] = __uint_as_float(raw[r][i].x << 16);
-        x[4 * i + 1] = __uint_as_float(raw[r][i].x & 0xFFFF0000u);
-        x[4 * i + 2] = __uint_as_float(raw[r][i].y << 16);
-        x[4 * i + 3] = __uint_as_float(raw[r][i].y & 0xFFFF0000u);
+        x[4 * i] = __uint_as_float(raw[0][i].x << 16);
+        x[4 * i + 1] = __uint_as_float(raw[0][i].x & 0xFFFF0000u);
+        x[4 * i + 2] = __uint_as_float(raw[0][i].y << 16);
+        x[4 * i + 3] = __uint_as_float(raw[0][i].y & 0xFFFF0000u);
+#pragma unroll
+        for (int r = 0; r + 1 < NT; ++r) raw[r][i] = raw[r + 1][i];
       }
 #pragma unroll
       for (int i = 0; i < E; ++i) {
