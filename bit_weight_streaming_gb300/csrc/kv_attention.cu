@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
 // The kernel and its n8 tiles for a request's rows. A warp of attn_kernel holds
 // O for every dimension, NT * D <= 512; more rows of a wide head go to the other
 // kernel, up to 64 at a time (at 48 rows of 256 attn_kernel's three passes over
-// the cache took 112 us for 100001 tokens, the wide kernel 70); what is still
+// the cache took 112 us for 100001 tokens, the wide kernel 68); what is still
 // more goes in groups, each of which reads the cache again.
 struct Form {
   bool wide;
