@@ -54,6 +54,19 @@ def _check_heads(name, t, rows, heads, dim):
     return row, head
 
 
+def _row_stride(name, t):
+    """Elements from row to row of a matrix whose rows may lie apart but not on each other (as expand() makes them)."""
+    rows, wide = t.shape
+    if t.stride(1) != 1 and wide > 1:
+        raise BwsError(f"{name} must be contiguous in its last dimension")
+    if rows <= 1:
+        return wide               # one row has no stride of its own
+    if t.stride(0) < wide:
+        raise BwsError(f"{name}'s rows of {wide} lie {t.stride(0)} apart: they must not overlap (a broadcast matrix "
+                       "needs contiguous())")
+    return t.stride(0)
+
+
 def _fail(rc, what):
     if rc:
         check(rc, what)
@@ -214,19 +227,23 @@ def kv_attention(q, cache, block_table, row_start, kv_lens, max_rows, scale=None
 def draft_verify(target, tokens, row_start, accept_u, sample_u, max_rows, draft=None):
     """Which drafted tokens stand against the target's probabilities, and the
     token drawn after them, from given uniform numbers. target fp32 [rows,
-    vocab]; draft fp32 [rows, vocab] or None (each draft was certain); tokens
+    vocab]; draft fp32 [rows, vocab] or None (each draft was certain), rows of
+    both at any stride of vocab or more; tokens
     int32 [rows] (the last row of a request has no draft), accept_u fp32
     [rows], row_start int32 [requests + 1], sample_u fp32 [requests]. Returns
     (out int32 [requests, max_rows]: the drafts that stand, the drawn token,
     then -1; n_out int32 [requests])."""
     T, V = target.shape
     R = sample_u.shape[0]
-    strides = [0, 0]
-    for i, t in enumerate((target, draft)):
-        if t is not None:
-            if t.dtype is not _F32 or t.shape != (T, V) or not t.is_cuda or (t.stride(1) != 1 and V > 1):
-                raise BwsError(f"target and draft must be CUDA fp32 tensors [{T}, {V}] with a contiguous last dimension")
-            strides[i] = max(t.stride(0), V)    # one row has no stride of its own
+    target_stride = _row_stride("target", target)
+    draft_stride = 0
+    if draft is not None:
+        if draft.shape != (T, V):
+            raise BwsError(f"draft must have target's shape [{T}, {V}]; it is {tuple(draft.shape)}")
+        draft_stride = _row_stride("draft", draft)
+    for t in (target, draft):
+        if t is not None and (t.dtype is not _F32 or not t.is_cuda):
+            raise BwsError(f"target and draft must be CUDA fp32 tensors; one is {t.dtype} on {t.device}")
     rows = (T,)
     _check("tokens", tokens, _I32, rows)
     _check("accept_u", accept_u, _F32, rows)
@@ -236,8 +253,8 @@ def draft_verify(target, tokens, row_start, accept_u, sample_u, max_rows, draft=
         raise BwsError("max_rows must be positive")
     out = torch.empty((R, max_rows), dtype=_I32, device=target.device)
     n_out = torch.empty_like(sample_u, dtype=_I32)
-    _fail(lib().bws_draft_verify(target.data_ptr(), strides[0], None if draft is None else draft.data_ptr(), strides[1],
-                                 tokens.data_ptr(), T, V, row_start.data_ptr(), R, accept_u.data_ptr(),
+    _fail(lib().bws_draft_verify(target.data_ptr(), target_stride, None if draft is None else draft.data_ptr(),
+                                 draft_stride, tokens.data_ptr(), T, V, row_start.data_ptr(), R, accept_u.data_ptr(),
                                  sample_u.data_ptr(), max_rows, out.data_ptr(), n_out.data_ptr(),
                                  _raw_stream(target.get_device())), "bws_draft_verify")
     return out, n_out

@@ -121,6 +121,26 @@ def test_python_refuses_cpu_tensors():
         bws.kv_plan(i, i, 16, torch.zeros((1, 4), dtype=torch.int32), i, i, 4)
 
 
+def test_python_refuses_overlapping_rows():
+    """A broadcast matrix is one row of memory: taken for a row each, its rows would be read past the end of it."""
+    import torch
+    import bit_weight_streaming_gb300 as bws
+    p, one = torch.zeros((5, 100)), torch.zeros((1, 100))
+    i, u = torch.zeros(5, dtype=torch.int32), torch.zeros(5)
+    start = torch.tensor([0, 5], dtype=torch.int32)
+    for target, draft in ((p, one.expand(5, 100)), (one.expand(5, 100), None), (p.view(-1).as_strided((5, 100), (60, 1)), p)):
+        with pytest.raises(bws.BwsError, match="lie (0|60) apart"):
+            bws.draft_verify(target, i, start, u, u[:1], 5, draft=draft)
+    with pytest.raises(bws.BwsError, match="last dimension"):
+        bws.draft_verify(torch.zeros((100, 5)).t(), i, start, u, u[:1], 5)
+    from bit_weight_streaming_gb300.serving import _row_stride
+    assert _row_stride("p", p) == 100 and _row_stride("p", p[::2]) == 200 and _row_stride("p", p[:, 3:90]) == 100
+    assert _row_stride("p", one.expand(1, 100)) == 100 and _row_stride("p", one.as_strided((1, 100), (7, 1))) == 100
+    assert _row_stride("p", torch.zeros((0, 100))) == 100 and _row_stride("p", torch.zeros((5, 1))) == 1
+    with pytest.raises(bws.BwsError):
+        _row_stride("p", torch.zeros((1, 1)).expand(5, 1))
+
+
 def test_oracle_scale():
     assert S.scale_for(448.0) == 1.0 and S.scale_for(448.5) == 2.0 and S.scale_for(224.0) == 0.5
     assert S.scale_for(0.0) == 2.0 ** -60 and S.scale_for(1e30) == 2.0 ** 60
