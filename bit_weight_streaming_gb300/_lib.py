@@ -45,6 +45,7 @@ SIGNATURES = {
     "bws_decode_step_tap_size": (Z, [P]),
     "bws_decode_step_tap": (I, [P, P, P, P, Z, P, Z, P]),
     "bws_kv_plan": (I, [P, P, I, I, P, I, P, P, I, P, P, P, P, P, P, P]),
+    "bws_kv_plan_bounded": (I, [P, P, I, I, P, I, P, I, P, I, P, P, P, P, P, P, P]),
     "bws_qk_norm_rope_append": (I, [P, P, P, P]),
     "bws_kv_attention_workspace_size": (Z, [I, I, I, I]),
     "bws_kv_attention": (I, [P, L, L, I, I, P, P, I, I, P, P, I, F, P, P, P, Z, P]),

@@ -34,6 +34,7 @@ struct PlanParams {
   int32_t* table;
   int max_blocks;
   const int32_t* free_blocks;
+  int n_list;   // entries of free_blocks: *n_free, read here, may not be trusted with them
   const int32_t* n_free;
   int n_rows;
   int32_t *slots, *positions, *row_start, *kv_lens, *n_free_out, *status;
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
   pdl_launch_dependents();
   pdl_wait();
   if (tid == 0) s_over = 0;
-  const int n_free = max(*p.n_free, 0);
+  const int n_given = *p.n_free, n_free = min(max(n_given, 0), p.n_list);
   const int per = (p.R + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
   long long rows = 0, blks = 0;
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
     if (tid == 0) {
       *p.n_free_out = max(n_free - taken, 0);
       *p.status = (taken > n_free ? BWS_KV_NO_BLOCKS : 0) | (s_over ? BWS_KV_TABLE_FULL : 0) |
-                  (total > p.n_rows ? BWS_KV_NO_ROWS : 0);
+                  (total > p.n_rows ? BWS_KV_NO_ROWS : 0) | (n_given > p.n_list ? BWS_KV_LIST_SHORT : 0);
     }
   }
   const int step = gridDim.x * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
@@ -689,12 +690,20 @@ int bws_kv_plan(const int32_t* seq_lens, const int32_t* new_lens, int n_requests
                 int32_t* block_table, int max_blocks, const int32_t* free_blocks, const int32_t* n_free, int n_rows,
                 int32_t* slots, int32_t* positions, int32_t* row_start, int32_t* kv_lens, int32_t* n_free_out,
                 int32_t* status, void* stream) {
+  return bws_kv_plan_bounded(seq_lens, new_lens, n_requests, block_tokens, block_table, max_blocks, free_blocks,
+                             INT32_MAX, n_free, n_rows, slots, positions, row_start, kv_lens, n_free_out, status, stream);
+}
+
+int bws_kv_plan_bounded(const int32_t* seq_lens, const int32_t* new_lens, int n_requests, int block_tokens,
+                        int32_t* block_table, int max_blocks, const int32_t* free_blocks, int n_list,
+                        const int32_t* n_free, int n_rows, int32_t* slots, int32_t* positions, int32_t* row_start,
+                        int32_t* kv_lens, int32_t* n_free_out, int32_t* status, void* stream) {
   using namespace bws;
   const char* name = "bws_kv_plan";
   if (n_requests < 0 || n_requests > kPlanMaxRequests)
     return fail(BWS_ERR_INVALID_ARG, "%s: n_requests = %d must be in [0, %d]", name, n_requests, kPlanMaxRequests);
-  if (n_rows < 0 || max_blocks < 0)
-    return fail(BWS_ERR_INVALID_ARG, "%s: n_rows = %d, max_blocks = %d", name, n_rows, max_blocks);
+  if (n_rows < 0 || max_blocks < 0 || n_list < 0)
+    return fail(BWS_ERR_INVALID_ARG, "%s: n_rows = %d, max_blocks = %d, n_list = %d", name, n_rows, max_blocks, n_list);
   if (block_tokens < 16 || block_tokens > 256 || block_tokens % 16 != 0)
     return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: block_tokens = %d must be a multiple of 16 in [16, 256]", name,
                 block_tokens);
@@ -706,8 +715,8 @@ int bws_kv_plan(const int32_t* seq_lens, const int32_t* new_lens, int n_requests
                         n_free_out, status};
   for (const void* q : ptrs)
     if (!aligned(q, 4)) return fail(BWS_ERR_MISALIGNED, "%s: 4-byte alignment needed", name);
-  PlanParams p = {seq_lens, new_lens, n_requests, block_tokens, block_table, max_blocks, free_blocks, n_free, n_rows,
-                  slots, positions, row_start, kv_lens, n_free_out, status,
+  PlanParams p = {seq_lens, new_lens, n_requests, block_tokens, block_table, max_blocks, free_blocks, n_list, n_free,
+                  n_rows, slots, positions, row_start, kv_lens, n_free_out, status,
                   aligned(slots, 16) && aligned(positions, 16)};
   static std::atomic<unsigned long long> attr{0};
   const cudaError_t e = set_smem_once(attr, plan_kernel, (int)sizeof(int) * (3 * kPlanMaxRequests + 2));

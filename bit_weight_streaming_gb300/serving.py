@@ -138,10 +138,11 @@ def kv_plan(seq_lens, new_lens, block_tokens, block_table, free_blocks, n_free, 
     kv_lens = torch.empty_like(seq_lens)
     n_out = torch.empty_like(n_free)
     status = torch.empty_like(n_free)
-    _fail(lib().bws_kv_plan(seq_lens.data_ptr(), new_lens.data_ptr(), R, block_tokens, block_table.data_ptr(), wide,
-                            free_blocks.data_ptr(), n_free.data_ptr(), n_rows, slots.data_ptr(), positions.data_ptr(),
-                            row_start.data_ptr(), kv_lens.data_ptr(), n_out.data_ptr(), status.data_ptr(),
-                            _raw_stream(seq_lens.get_device())), "bws_kv_plan")
+    _fail(lib().bws_kv_plan_bounded(seq_lens.data_ptr(), new_lens.data_ptr(), R, block_tokens, block_table.data_ptr(),
+                                    wide, free_blocks.data_ptr(), free_blocks.numel(), n_free.data_ptr(), n_rows,
+                                    slots.data_ptr(), positions.data_ptr(), row_start.data_ptr(), kv_lens.data_ptr(),
+                                    n_out.data_ptr(), status.data_ptr(), _raw_stream(seq_lens.get_device())),
+          "bws_kv_plan")
     return KvPlan(slots, positions, row_start, kv_lens, n_out, status)
 
 

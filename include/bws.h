@@ -465,7 +465,9 @@ typedef struct bws_kv_cache {
 enum bws_kv_plan_status {  /* bits of bws_kv_plan's status                     */
   BWS_KV_NO_BLOCKS = 1,    /* the free list ran out: entries and slots are -1  */
   BWS_KV_TABLE_FULL = 2,   /* a request is longer than its table row           */
-  BWS_KV_NO_ROWS = 4       /* more new tokens than n_rows                      */
+  BWS_KV_NO_ROWS = 4,      /* more new tokens than n_rows                      */
+  BWS_KV_LIST_SHORT = 8    /* n_free is more than the list has (the bounded
+                              form): taken as the list's length                */
 };
 
 /* Block tables and slot maps from request lengths, on the device. Request r
@@ -490,6 +492,16 @@ int bws_kv_plan(const int32_t* seq_lens, const int32_t* new_lens, int n_requests
                 int32_t* slots, int32_t* positions, int32_t* row_start,
                 int32_t* kv_lens, int32_t* n_free_out, int32_t* status,
                 void* stream);
+
+/* bws_kv_plan for a free list of n_list entries (>= 0): n_free, which only the
+ * device knows, is held to them, so that no entry past the list is read.
+ * bws_kv_plan itself reads as many as n_free says. */
+int bws_kv_plan_bounded(const int32_t* seq_lens, const int32_t* new_lens, int n_requests,
+                        int block_tokens, int32_t* block_table, int max_blocks,
+                        const int32_t* free_blocks, int n_list, const int32_t* n_free, int n_rows,
+                        int32_t* slots, int32_t* positions, int32_t* row_start,
+                        int32_t* kv_lens, int32_t* n_free_out, int32_t* status,
+                        void* stream);
 
 /* Per-head RMS norm of queries and keys, their rotation by position, and the
  * write of keys and values into the cache, in one pass. Per head, in FP32:

@@ -1,0 +1,34 @@
+"""The serving entry points on the GPU at the edges of their contracts: lists and tables that run short, rows beyond
+what a call takes, tokens far apart in weight, lengths near 2^31."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import bws, device, f64, np_
+from oracle import formats as F, serving as S
+from test_gpu_serving import attention_case, check_append, check_plan, check_verify, freqs, gen, held, ints, make_cache, \
+    rows, verify_case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    return bws()
+
+
+# ---- block tables ----------------------------------------------------------------
+
+def test_plan_free_count_past_its_list(m):
+    """A count of free blocks that the list does not have is held to the list and reported."""
+    new, table = [40, 100], ints([[-1] * 8, [-1] * 8])
+    free = [5, 9, 2, 7]
+    p = m.kv_plan(ints([0, 0]), ints(new), 16, table, ints(free), ints([5000]), sum(new))
+    torch.cuda.synchronize()
+    want = S.kv_plan([0, 0], new, 16, [[-1] * 8, [-1] * 8], free, 4, sum(new))
+    for g, w in zip((table, p.slots, p.positions, p.row_start, p.kv_lens), want):
+        assert np.array_equal(np_(g), np.asarray(w))
+    assert p.n_free.item() == 0 and p.status.item() == want[6] | 8
+    p = m.kv_plan(ints([0, 0]), ints([16, 16]), 16, table, ints(free), ints([5]), 32)
+    torch.cuda.synchronize()
+    assert p.n_free.item() == 2 and p.status.item() == 8

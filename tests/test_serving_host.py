@@ -37,6 +37,8 @@ def test_plan_refusals(lib):
     assert b"null" in lib.bws_last_error()
     assert call(out=16) == 1 and b"n_free_out" in lib.bws_last_error()
     assert call(seq=18) == 3 and call(status=17) == 3
+    assert lib.bws_kv_plan_bounded(16, 16, 1, 16, 16, 4, 16, -1, 16, 8, 16, 16, 16, 16, 32, 16, None) == 1
+    assert b"n_list" in lib.bws_last_error()
 
 
 @pytest.mark.parametrize("bad,code", [
