@@ -708,13 +708,14 @@ int bws_kv_plan_bounded(const int32_t* seq_lens, const int32_t* new_lens, int n_
     return fail(BWS_ERR_UNSUPPORTED_SHAPE, "%s: block_tokens = %d must be a multiple of 16 in [16, 256]", name,
                 block_tokens);
   if (!n_free || !row_start || !n_free_out || !status || (n_requests > 0 && (!seq_lens || !new_lens || !kv_lens)) ||
-      (n_requests > 0 && max_blocks > 0 && (!block_table || !free_blocks)) || (n_rows > 0 && (!slots || !positions)))
+      (n_requests > 0 && max_blocks > 0 && !block_table) || (n_rows > 0 && (!slots || !positions)))
     return fail(BWS_ERR_INVALID_ARG, "%s: null pointer", name);
   if (n_free == n_free_out) return fail(BWS_ERR_INVALID_ARG, "%s: n_free_out must not be n_free", name);
   const void* ptrs[] = {seq_lens, new_lens, block_table, free_blocks, n_free, slots, positions, row_start, kv_lens,
                         n_free_out, status};
   for (const void* q : ptrs)
     if (!aligned(q, 4)) return fail(BWS_ERR_MISALIGNED, "%s: 4-byte alignment needed", name);
+  if (free_blocks == nullptr) n_list = 0;   // an empty list has no address
   PlanParams p = {seq_lens, new_lens, n_requests, block_tokens, block_table, max_blocks, free_blocks, n_list, n_free,
                   n_rows, slots, positions, row_start, kv_lens, n_free_out, status,
                   aligned(slots, 16) && aligned(positions, 16)};

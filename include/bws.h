@@ -479,7 +479,7 @@ enum bws_kv_plan_status {  /* bits of bws_kv_plan's status                     *
  * without a block, get slot -1 (position -1 past the last row), which
  * bws_qk_norm_rope_append skips.
  *   seq_lens, new_lens int32 [n_requests]; block_table int32
- *   [n_requests][max_blocks] in/out; free_blocks int32 (n_free entries);
+ *   [n_requests][max_blocks] in/out; free_blocks int32 (n_free entries; NULL: none);
  *   n_free int32 [1]; slots, positions int32 [n_rows] out; row_start int32
  *   [n_requests + 1] out; kv_lens int32 [n_requests] out (seq + new);
  *   n_free_out int32 [1] out (not n_free itself); status int32 [1] out

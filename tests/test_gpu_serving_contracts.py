@@ -32,3 +32,15 @@ def test_plan_free_count_past_its_list(m):
     p = m.kv_plan(ints([0, 0]), ints([16, 16]), 16, table, ints(free), ints([5]), 32)
     torch.cuda.synchronize()
     assert p.n_free.item() == 2 and p.status.item() == 8
+
+
+def test_plan_empty_free_list(m):
+    """Nothing is free and no list is there: rows that fit into held blocks get their slots."""
+    table = ints([[7, -1, -1], [4, -1, -1]])
+    p = m.kv_plan(ints([3, 15]), ints([20, 1]), 16, table, ints([]), ints([0]), 22)
+    torch.cuda.synchronize()
+    want = S.kv_plan([3, 15], [20, 1], 16, [[7, -1, -1], [4, -1, -1]], [], 0, 22)
+    for g, w in zip((table, p.slots, p.positions, p.row_start, p.kv_lens), want):
+        assert np.array_equal(np_(g), np.asarray(w))
+    assert p.n_free.item() == 0 and p.status.item() == want[6] == 1
+    assert p.slots.tolist()[:13] == [7 * 16 + 3 + i for i in range(13)] and p.slots.tolist()[13:] == [-1] * 7 + [4 * 16 + 15, -1]
