@@ -77,10 +77,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
     const uint32_t have = blocks_of(seq, p.B), need = blocks_of(seq + nw, p.B);
     s_row[r] = (int)nw;
     s_seq[r] = (int)seq;
-    s_blk[r] = (int)(need - have);
+    const uint32_t most = (uint32_t)p.max_blocks;   // what the table row cannot hold is not taken
+    const uint32_t take = min(need, most) - min(have, most);
+    s_blk[r] = (int)take;
     rows += nw;
-    blks += need - have;
-    over |= need > (uint32_t)p.max_blocks;
+    blks += take;
+    over |= need > most;
   }
   long long ir = rows, ib = blks;
 #pragma unroll
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
   for (long long i = first; i < taken; i += step) {
     const int r = last_not_above(s_blk, p.R, (int)i);
     const long long c = blocks_of(s_seq[r], p.B) + (i - s_blk[r]);
-    if (c < p.max_blocks) p.table[(size_t)r * p.max_blocks + c] = i < n_free ? p.free_blocks[n_free - 1 - i] : -1;
+    p.table[(size_t)r * p.max_blocks + c] = i < n_free ? p.free_blocks[n_free - 1 - i] : -1;
   }
   // Four rows a thread: B is a multiple of 16, so a thread whose rows belong to
   // one request meets at most two blocks.

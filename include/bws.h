@@ -464,10 +464,11 @@ typedef struct bws_kv_cache {
 
 enum bws_kv_plan_status {  /* bits of bws_kv_plan's status                     */
   BWS_KV_NO_BLOCKS = 1,    /* the free list ran out: entries and slots are -1  */
-  BWS_KV_TABLE_FULL = 2,   /* a request is longer than its table row           */
+  BWS_KV_TABLE_FULL = 2,   /* a request is longer than its table row: it takes
+                              the blocks that the row holds, and no slots past */
   BWS_KV_NO_ROWS = 4,      /* more new tokens than n_rows                      */
-  BWS_KV_LIST_SHORT = 8    /* n_free is more than the list has (the bounded
-                              form): taken as the list's length                */
+  BWS_KV_LIST_SHORT = 8    /* n_free is more than the list has (bounded form,
+                              or no list): taken as the list's length          */
 };
 
 /* Block tables and slot maps from request lengths, on the device. Request r

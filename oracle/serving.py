@@ -16,13 +16,12 @@ def kv_plan(seq_lens, new_lens, block_tokens, table, free_blocks, n_free, n_rows
         seq, new = max(int(seq), 0), max(int(new), 0)
         have, need = -(-seq // B), -(-(seq + new) // B)
         got = {}
-        for c in range(have, need):
+        for c in range(have, min(need, wide)):   # a block that the table row cannot hold is not taken
             got[c] = int(free_blocks[n_free - 1 - taken]) if taken < n_free else -1
             if taken >= n_free:
                 status |= 1
             taken += 1
-            if c < wide:
-                table[r, c] = got[c]
+            table[r, c] = got[c]
         if need > wide:
             status |= 2
         for j in range(new):

@@ -44,3 +44,22 @@ def test_plan_empty_free_list(m):
         assert np.array_equal(np_(g), np.asarray(w))
     assert p.n_free.item() == 0 and p.status.item() == want[6] == 1
     assert p.slots.tolist()[:13] == [7 * 16 + 3 + i for i in range(13)] and p.slots.tolist()[13:] == [-1] * 7 + [4 * 16 + 15, -1]
+
+
+@pytest.mark.parametrize("seq,new,wide,n_free", [
+    ([0, 0], [80, 16], 2, 8), ([0, 0], [80, 16], 2, 3), ([20, 3], [40, 40], 3, 5), ([70, 0], [16, 16], 2, 4),
+    ([15, 0, 100], [100, 33, 1], 4, 9)])
+def test_plan_takes_only_what_tables_hold(m, seq, new, wide, n_free):
+    """A request longer than its table row takes no block that the row cannot hold, and none from those behind it."""
+    check_plan(m, seq, new, 16, wide, n_free, sum(new))
+    table = torch.full((len(seq), wide), -1, dtype=torch.int32, device=device())
+    for r, s in enumerate(seq):
+        have = min(-(-s // 16), wide)
+        table[r, :have] = 900 + torch.arange(have, dtype=torch.int32, device=device())
+    before = table.clone()
+    p = m.kv_plan(ints(seq), ints(new), 16, table, ints(list(range(n_free))), ints([n_free]), sum(new))
+    torch.cuda.synchronize()
+    stored = ((table != before) & (table >= 0)).sum().item()
+    wanted = sum(min(-(-(s + n) // 16), wide) - min(-(-s // 16), wide) for s, n in zip(seq, new))
+    assert n_free - p.n_free.item() == stored == min(wanted, n_free)
+    assert p.status.item() & 2 and bool(p.status.item() & 1) == (wanted > n_free)

@@ -156,6 +156,13 @@ def test_oracle_plan_by_hand():
     assert start.tolist() == [0, 2, 3] and kv.tolist() == [17, 1] and n == 1 and st == 0
 
 
+def test_oracle_plan_loses_no_block():
+    # the first request's row holds two of the five blocks it needs: three stay free, and the second gets its own
+    t, slots, _, _, kv, n, st = S.kv_plan([0, 0], [80, 16], 16, [[-1, -1], [-1, -1]], list(range(8)), 8, 96)
+    assert t.tolist() == [[7, 6], [5, -1]] and n == 5 and st == 2 and kv.tolist() == [80, 16]
+    assert (slots[:32] >= 0).all() and (slots[32:80] == -1).all() and slots[80:].tolist() == list(range(80, 96))
+
+
 def test_oracle_append_grows_and_rounds_again():
     codes = np.zeros((1, 1, 16, 64), dtype=np.uint8)
     scale = np.ones((1, 1), dtype=np.float32)
