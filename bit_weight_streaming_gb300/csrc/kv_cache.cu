@@ -717,6 +717,9 @@ int bws_kv_plan_bounded(const int32_t* seq_lens, const int32_t* new_lens, int n_
                         n_free_out, status};
   for (const void* q : ptrs)
     if (!aligned(q, 4)) return fail(BWS_ERR_MISALIGNED, "%s: 4-byte alignment needed", name);
+  // CTAs read every length while another writes kv_lens
+  if (n_requests > 0 && (kv_lens == seq_lens || kv_lens == new_lens))
+    return fail(BWS_ERR_INVALID_ARG, "%s: kv_lens must not be seq_lens or new_lens", name);
   if (free_blocks == nullptr) n_list = 0;   // an empty list has no address
   PlanParams p = {seq_lens, new_lens, n_requests, block_tokens, block_table, max_blocks, free_blocks, n_list, n_free,
                   n_rows, slots, positions, row_start, kv_lens, n_free_out, status,

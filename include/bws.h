@@ -482,7 +482,8 @@ enum bws_kv_plan_status {  /* bits of bws_kv_plan's status                     *
  *   seq_lens, new_lens int32 [n_requests]; block_table int32
  *   [n_requests][max_blocks] in/out; free_blocks int32 (n_free entries; NULL: none);
  *   n_free int32 [1]; slots, positions int32 [n_rows] out; row_start int32
- *   [n_requests + 1] out; kv_lens int32 [n_requests] out (seq + new);
+ *   [n_requests + 1] out; kv_lens int32 [n_requests] out (seq + new; not an
+ *   input itself);
  *   n_free_out int32 [1] out (not n_free itself); status int32 [1] out
  *   (bws_kv_plan_status bits). All device pointers.
  * 0 <= n_requests <= 4096, n_rows >= 0, block_tokens as bws_kv_cache. The call

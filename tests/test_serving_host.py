@@ -24,6 +24,15 @@ def cache(**kw):
     return _KvCache(*v.values())
 
 
+def test_plan_refuses_lengths_in_place(lib):
+    """CTAs read the lengths while another writes kv_lens."""
+    def call(seq, new, kv):
+        return lib.bws_kv_plan(seq, new, 1, 16, 16, 4, 16, 16, 8, 16, 16, 16, kv, 32, 16, None)
+
+    for lens in ((64, 128, 64), (64, 128, 128)):
+        assert call(*lens) == 1 and b"kv_lens" in lib.bws_last_error()
+
+
 def test_plan_refusals(lib):
     f = lib.bws_kv_plan
 
