@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     const Request& rq = cur.rq;
     const int row0 = cur.row0, head = cur.head;
     const int n_group_rows = min(rq.rows * p.G - row0, S::kRows);
-    const int seen0 = rq.kv - rq.rows;   // row j sees tokens <= seen0 + j
+    const int seen0 = rq.seen0;   // row j sees tokens <= seen0 + j
     uint32_t* const nan_mask = T.nan_mask[turn];
 
     uint32_t qf[S::kQInRegs ? kMT : 1][S::kQInRegs ? NT : 1][2];
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
               for (int k = 0; k < 4; ++k)
                 if (((word >> (8 * k)) & 0x7Fu) == 0x7Fu) {
                   word &= ~(0xFFu << (8 * k));
-                  atomicOr(&nan_mask[byte + k], 1u << own);
+                  atomicOr(&nan_mask[byte + k], 1u << min(own, 31));
                 }
             }
             asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(word) : "memory");

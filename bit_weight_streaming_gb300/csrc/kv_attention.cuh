@@ -57,13 +57,16 @@ BWS_DEV int block_index(const AttnParams& p, int token) {
 }
 
 struct Request {
-  int rows, start, kv, units, groups;   // kv: cached tokens; units of one segment; row groups
+  int rows, start, kv, units, groups;   // kv: tokens that the table row can hold; units of one segment; row groups
+  int seen0;                            // the last token that row 0 sees; row j sees j more
 };
 
 BWS_DEV Request request_from(const AttnParams& p, int begin, int end, int kv, int group_rows) {
   Request q;
   q.start = min(max(begin, 0), p.n_rows);
-  q.rows = min(max(end - q.start, 0), min(p.max_rows, p.n_rows - q.start));
+  const int rows = max(min(end, p.n_rows) - q.start, 0);
+  q.rows = min(rows, p.max_rows);
+  q.seen0 = max(kv, 0) - rows;   // by the request's own length, where the table is too short for it as well
   const long long cap = (long long)p.max_blocks * p.B;
   q.kv = (int)min((long long)max(kv, 0), cap);
   q.units = max(1, (q.kv + p.unit - 1) / p.unit);   // a request without tokens still writes its rows

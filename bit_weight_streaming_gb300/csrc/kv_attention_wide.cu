@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     const Segment& cur = T.seg[turn];
     const Request& rq = cur.rq;
     const int tiles = cur.last - cur.first;
-    const int seen0 = rq.kv - rq.rows;   // row j sees tokens <= seen0 + j
+    const int seen0 = rq.seen0;          // row j sees tokens <= seen0 + j
     uint32_t* const nan_mask = T.nan_mask[turn];
     float o[S::kMT][NT][4];              // the value warps'
     const int g = lane >> 2, t4 = lane & 3;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
         scales_of(block_n, ks_n, vs_n);
         block_n = block_of(i + 2);
         const float lvs = log2f(vs), rvs = 1.0f / vs;
-        const int tok = (cur.first + i) * kWideTile + token, own = tok - seen0;
+        const int tok = (cur.first + i) * kWideTile + token, own = min(tok - seen0, 31);
         const bool there = ks != -1.0f && tok < rq.kv;
         // rows below `hidden` do not see the token: the j-th token of the rows'
         // own is seen from row j on
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
                 for (int k = 0; k < 4; ++k)
                   if (((word >> (8 * k)) & 0x7Fu) == 0x7Fu) {
                     word &= ~(0xFFu << (8 * k));
-                    atomicOr(&nan_mask[byte + k], 1u << its);
+                    atomicOr(&nan_mask[byte + k], 1u << min(its, 31));
                   }
               }
               asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(word) : "memory");

@@ -546,7 +546,7 @@ int bws_qk_norm_rope_append(const bws_qkv* in, const bws_kv_cache* cache,
  * tokens, already in the cache). Query head h reads kv head h / (n_q_heads /
  * n_kv_heads). A row that sees no token gives 0 (lse -inf). Codes are exact in
  * the products; sums and softmax statistics are FP32. Table entries outside
- * the cache count as tokens that are not there.
+ * the cache, and tokens past the table row, count as tokens that are not there.
  *   q bf16 [n_rows][n_q_heads][head_dim], innermost contiguous, strides in
  *   elements (multiples of 8), 16-byte aligned; block_table int32 [n_requests]
  *   [max_blocks]; row_start int32 [n_requests + 1]; kv_lens int32

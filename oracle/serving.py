@@ -116,10 +116,11 @@ def attention(q, k_codes, v_codes, k_scale, v_scale, table, row_start, kv_lens, 
     seen = np.zeros((T, H))
     for r, length in enumerate(kv_lens):
         a, b = int(row_start[r]), int(row_start[r + 1])
-        length = min(max(int(length), 0), table.shape[1] * B)
+        length = max(int(length), 0)
         if b <= a:
             continue
-        toks = [t for t in range(length) if 0 <= table[r, t // B] < n_blocks]
+        # what the table cannot hold is not there; the rows' sight goes by the length all the same
+        toks = [t for t in range(min(length, table.shape[1] * B)) if 0 <= table[r, t // B] < n_blocks]
         blk = np.array([table[r, t // B] for t in toks], dtype=np.int64)
         at = np.array([t % B for t in toks], dtype=np.int64)
         toks = np.array(toks, dtype=np.int64)

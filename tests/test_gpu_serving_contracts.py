@@ -63,3 +63,40 @@ def test_plan_takes_only_what_tables_hold(m, seq, new, wide, n_free):
     wanted = sum(min(-(-(s + n) // 16), wide) - min(-(-s // 16), wide) for s, n in zip(seq, new))
     assert n_free - p.n_free.item() == stored == min(wanted, n_free)
     assert p.status.item() & 2 and bool(p.status.item() & 1) == (wanted > n_free)
+
+
+# ---- attention -----------------------------------------------------------------------
+
+def check_result(got, gl, want, want_lse, size, score, D):
+    """The bound per output: weights in f16 (2^-11), the scores' FP32 sums (D roundings of 2^-24 of the absolute sum, in
+    weight and total), the exponents' arguments and remaining sums (2^-14), each of sum p |v|, and half a BF16 step.
+    Nothing of it grows with the tokens."""
+    delta = D * 2.0 ** -24 * score
+    lim = (2.0 ** -11 + 2.0 ** -14 + 2 * delta)[..., None] * size + 0.5 * F.bf16_ulp(np.maximum(np.abs(want), np.abs(got)))
+    err = np.abs(got - want)
+    assert (err <= lim).all(), ((err > lim).sum(), (err / np.maximum(lim, 1e-300)).max())
+    fin = np.isfinite(want_lse)
+    assert np.array_equal(np.isfinite(gl), fin)
+    assert (np.abs(gl[fin] - want_lse[fin]) <= delta[fin] + 2.0 ** -18 * (1 + np.abs(want_lse[fin]))).all()
+
+
+def check_rows(q, c, table, start, kv, scale, out, lse, which):
+    """Rows `which` of a result against the oracle."""
+    want, want_lse, (size, score, _, _) = S.attention(f64(q), np_(c.k), np_(c.v), np_(c.k_scale), np_(c.v_scale),
+                                                      np.asarray(table), start, kv, scale)
+    check_result(*(x[which] for x in (f64(out), f64(lse), want, want_lse, size, score)), q.shape[2])
+
+
+@pytest.mark.parametrize("D,H,K,n", [(64, 4, 2, 4), (128, 4, 2, 4), (256, 4, 1, 4), (256, 24, 4, 8), (128, 32, 2, 8)])
+@pytest.mark.parametrize("past", [1, 3, 9, 100, 2 ** 31 - 1])
+def test_attention_longer_than_its_table(m, D, H, K, n, past):
+    """Tokens past the table row are not there; the rows' sight goes by the request's length all the same."""
+    B, held_tokens = 16, 160
+    c, q, t, s, mx = attention_case(m, D, H, K, B, [n, 1], [held_tokens, 40], seed=n + D)
+    kv = [min(held_tokens + past, 2 ** 31 - 1), 40]
+    out, lse = m.kv_attention(q, c, ints(t), ints(s), ints(kv), mx, lse=True)
+    torch.cuda.synchronize()
+    for j in range(n):   # each row as a request of its own, of as many tokens as it sees
+        sees = min(kv[0] - n + j + 1, held_tokens)
+        check_rows(q[j:j + 1], c, t[:1], [0, 1], [sees], D ** -0.5, out[j:j + 1], lse[j:j + 1], slice(None))
+    check_rows(q[n:], c, t[1:], [0, 1], [40], D ** -0.5, out[n:], lse[n:], slice(None))

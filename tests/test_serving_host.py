@@ -197,6 +197,16 @@ def test_oracle_attention_closed_form():
     assert np.allclose(lse[:2, 0], [np.log(2), np.log(3)]) and lse[2, 0] == -np.inf
 
 
+def test_oracle_attention_longer_than_its_table():
+    # 40 tokens of which the table holds 32: both rows see all 32, the last token's value among equal scores too
+    k = np.zeros((2, 1, 16, 64), dtype=np.uint8)
+    v = np.zeros((2, 1, 16, 64), dtype=np.uint8)
+    v[1, 0, 15] = F.e4m3_encode(np.array([448.0]))
+    s = np.ones((2, 1), dtype=np.float32)
+    out, lse, _ = S.attention(np.ones((2, 1, 64)), k, v, s, s, np.array([[0, 1]]), [0, 2], [40], 0.125)
+    assert np.allclose(out, 14.0) and np.allclose(lse, np.log(32))
+
+
 def test_oracle_verify_draws_the_target():
     """Speculative sampling leaves the target's distribution: counted over a grid of uniform numbers."""
     p = np.array([[0.5, 0.25, 0.25], [1, 0, 0]], dtype=np.float32)
