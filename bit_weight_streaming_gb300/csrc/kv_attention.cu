@@ -77,7 +77,7 @@ struct __align__(16) Tail {
   unsigned long long full[kAttnWarps][Shape<D, NT>::kStages];
   long long line_warp[kAttnWarps];
   long long line_found[2];
-  uint32_t failed;
+  uint32_t status;
 };
 
 template <int D, int NT>
@@ -98,12 +98,12 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     for (int s = 0; s < S::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
     mbar_fence_init();
   }
-  if (tid == 0) T.failed = 0;
+  if (tid == 0) T.status = 0;
   pdl_launch_dependents();
   pdl_wait();
   const int cta = blockIdx.x;
   Walk walk;
-  walk.start(p, S::kRows, T.line_warp, T.line_found);
+  walk.start(p, S::kRows, T.line_warp, T.line_found, &T.status);
   const uint64_t pol = l2_evict_first();
   uint32_t phase_base = 0;   // units this warp has put through its ring
   bool dead = false;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
       if (!dead && !mbar_wait_bounded(bar0 + 8 * s, (it / S::kStages) & 1, kAttnPolls)) dead = true;
       if (__any_sync(0xffffffffu, dead)) {
         dead = true;
-        if (lane == 0) T.failed = 1;
+        if (lane == 0) atomicOr(&T.status, (uint32_t)BWS_STATUS_WAIT_TIMEOUT);
         for (int k = i + 1; k < min(i + S::kStages, mine); ++k) {   // the copies still on their way
           const uint32_t at = phase_base + k;
           mbar_wait_bounded(bar0 + 8 * (at % S::kStages), (at / S::kStages) & 1, kAttnPolls);
@@ -496,7 +496,20 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     turn ^= 1;
   }
   __syncthreads();
-  if (tid == 0) p.failed[cta] = T.failed;
+  if (tid == 0) p.failed[cta] = T.status;
+}
+
+// Rows [from, to) of the output become what a row without tokens is; the CTAs
+// of the grid take them in turn.
+template <int D>
+BWS_DEV void clear_rows(const AttnParams& p, int from, int to) {
+  const int n = gridDim.x * gridDim.y;
+  for (int row = from + blockIdx.y * gridDim.x + blockIdx.x; row < to; row += n) {
+    uint4* const out = reinterpret_cast<uint4*>(p.out + (size_t)row * p.H * D);
+    for (int i = threadIdx.x; i < p.H * (D / 8); i += blockDim.x) out[i] = make_uint4(0, 0, 0, 0);
+    if (p.lse != nullptr)
+      for (int i = threadIdx.x; i < p.H; i += blockDim.x) p.lse[(size_t)row * p.H + i] = -INFINITY;
+  }
 }
 
 // Joins the partial results of a cut segment, x: its number where the segments
@@ -513,17 +526,23 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   pdl_launch_dependents();
   pdl_wait();
   const int c = blockIdx.x;
+  const uint32_t status = p.failed[0];   // what is said of the requests every CTA says
   if (c == 0 && blockIdx.y == 0) {
     if (threadIdx.x == 0) s_bad = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < p.n_ctas; i += 256)
-      if (p.failed[i] != 0) s_bad = 1;
+      if (p.failed[i] != 0) atomicOr(&s_bad, p.failed[i]);
     __syncthreads();
     if (threadIdx.x == 0) {
       p.hdr[0] = 0;
-      p.hdr[1] = s_bad ? (uint32_t)BWS_STATUS_WAIT_TIMEOUT : 0u;
+      p.hdr[1] = s_bad;
     }
   }
+  if (status & BWS_STATUS_KV_ROWS)
+    for (int r = 0; r < p.R; ++r) {
+      const Request q = request_of(p, r, kRows);
+      clear_rows<D>(p, q.start + q.rows, q.start + q.rows + q.excess);
+    }
   const int4 cut = p.cut[2 * c];
   const int4 more = p.cut[2 * c + 1];
   if (p.by_segment) {   // a request's missing row groups have no entry

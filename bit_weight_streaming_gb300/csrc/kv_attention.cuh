@@ -40,7 +40,7 @@ struct AttnParams {
   int4* cut;          // [max(CTAs, segments)][2]: segments that other CTAs go on with
   int by_segment;     // cut's index: the segment, else the CTA that starts it
   int max_groups;     // row groups of a full request
-  uint32_t* failed;   // [CTAs]
+  uint32_t* failed;   // [CTAs]: bws_status_bits
   uint32_t* hdr;
   int n_ctas, least;  // CTAs; smallest share in units
   int lead;           // what a segment costs beside its units, in units
@@ -59,6 +59,7 @@ BWS_DEV int block_index(const AttnParams& p, int token) {
 struct Request {
   int rows, start, kv, units, groups;   // kv: tokens that the table row can hold; units of one segment; row groups
   int seen0;                            // the last token that row 0 sees; row j sees j more
+  int excess;                           // rows beyond max_rows
 };
 
 BWS_DEV Request request_from(const AttnParams& p, int begin, int end, int kv, int group_rows) {
@@ -66,6 +67,7 @@ BWS_DEV Request request_from(const AttnParams& p, int begin, int end, int kv, in
   q.start = min(max(begin, 0), p.n_rows);
   const int rows = max(min(end, p.n_rows) - q.start, 0);
   q.rows = min(rows, p.max_rows);
+  q.excess = rows - q.rows;
   q.seen0 = max(kv, 0) - rows;   // by the request's own length, where the table is too short for it as well
   const long long cap = (long long)p.max_blocks * p.B;
   q.kv = (int)min((long long)max(kv, 0), cap);
@@ -89,13 +91,20 @@ struct Line {
 };
 
 // The whole CTA: the line's length, the share, and the request at position
-// cta * share, if the line has it.
-BWS_DEV Line find_on_line(const AttnParams& p, int group_rows, int cta, long long* s_warp, long long* s_found) {
+// cta * share, if the line has it. s_status (set before) gains a bit where a
+// request has too many rows.
+BWS_DEV Line find_on_line(const AttnParams& p, int group_rows, int cta, long long* s_warp, long long* s_found,
+                          uint32_t* s_status) {
   const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.R + n - 1) / n;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += length_of(p, request_of(p, r, group_rows));
+  bool excess = false;
+  for (int r = r0; r < r1; ++r) {
+    const Request q = request_of(p, r, group_rows);
+    mine += length_of(p, q);
+    excess |= q.excess > 0;
+  }
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -104,6 +113,7 @@ BWS_DEV Line find_on_line(const AttnParams& p, int group_rows, int cta, long lon
   }
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
+  if (excess) atomicOr(s_status, (uint32_t)BWS_STATUS_KV_ROWS);
   long long before = inc - mine, total = 0;
   for (int w = 0; w < n / 32; ++w) {
     if (w < warp) before += s_warp[w];
@@ -156,9 +166,9 @@ struct Walk {
     next_kv = there ? p.kv_lens[r + 1] : 0;
   }
   // (the whole CTA)
-  BWS_DEV void start(const AttnParams& p, int group_rows, long long* s_warp, long long* s_found) {
+  BWS_DEV void start(const AttnParams& p, int group_rows, long long* s_warp, long long* s_found, uint32_t* s_status) {
     cta = blockIdx.x;
-    const Line line = find_on_line(p, group_rows, cta, s_warp, s_found);
+    const Line line = find_on_line(p, group_rows, cta, s_warp, s_found, s_status);
     share = line.share;
     u = u0 = cta * share;
     u1 = min(line.total, u0 + share);

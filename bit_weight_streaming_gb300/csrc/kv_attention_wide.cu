@@ -86,7 +86,7 @@ struct __align__(1024) WideTail {
   Segment seg[2];
   int more;
   uint32_t tmem;
-  uint32_t failed;
+  uint32_t status;
 };
 
 template <int D, int NT>
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
       mbar_init(p_free + 8 * b, kValueWarps);
     }
     mbar_init(smem_u32(&T.drain), 1);
-    T.failed = 0;
+    T.status = 0;
     mbar_fence_init();
   }
   fence_before();
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
   pdl_wait();
   {
     Walk walk;
-    walk.start(p, S::kRows, T.line_warp, T.line_found);   // its barriers publish the mbarriers and the TMEM address too
+    walk.start(p, S::kRows, T.line_warp, T.line_found, &T.status);   // its barriers publish the mbarriers and the TMEM address too
     if (tid == 0) {
       T.walk = walk;
       T.more = T.walk.next(p, S::kRows, T.seg[0]);
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
       }
     }
     if (dead && lane == 0) {
-      T.failed = 1;
+      atomicOr(&T.status, (uint32_t)BWS_STATUS_WAIT_TIMEOUT);
       // the copies still on their way
       for (int s = 0; s < S::kKStages; ++s)
         mbar_wait_bounded(k_full + 8 * s, (int)((phase_base / S::kKStages) & 1), kAttnPolls);
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     }
   }
   __syncthreads();
-  if (tid == 0) p.failed[blockIdx.x] = T.failed;
+  if (tid == 0) p.failed[blockIdx.x] = T.status;
   if (warp == kSoftWarps + kMmaWarp) {   // every product has finished before the columns are released
     if (lane == 0) {
       commit(smem_u32(&T.drain));

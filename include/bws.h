@@ -68,6 +68,8 @@ enum bws_status_bits {
                                    cores: an activation below 2^-19 of its
                                    token's largest magnitude was rounded to a
                                    multiple of 2^-26 of that magnitude       */
+  BWS_STATUS_KV_ROWS = 0x10u,   /* bws_kv_attention: a request has more rows
+                                   than max_rows; those past it are zero     */
   BWS_STATUS_WAIT_TIMEOUT = 0x100u /* a bounded device wait ran out: the
                                    results of that call are not valid        */
 };
@@ -554,8 +556,10 @@ int bws_qk_norm_rope_append(const bws_qkv* in, const bws_kv_cache* cache,
  *   [n_q_heads] (log of the sum of exponentials) or NULL. Device pointers; the
  *   lengths are read on the device, so a captured call follows them.
  * 1 <= max_rows <= 8 bounds the rows of a request, n_q_heads / n_kv_heads in
- * 1..16. Workspace: bws_kv_attention_workspace_size() bytes, 256-byte aligned;
- * bws_status_word reports a bounded wait that ran out. Two kernels. */
+ * 1..16. Of a request with more, the first max_rows are computed (their sight
+ * goes by all n_r), the others give 0 (lse -inf) and the status word says so.
+ * Workspace: bws_kv_attention_workspace_size() bytes, 256-byte aligned;
+ * bws_status_word also reports a bounded wait that ran out. Two kernels. */
 size_t bws_kv_attention_workspace_size(int n_q_heads, int n_kv_heads, int head_dim, int max_rows);
 int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride,
                      int n_rows, int n_q_heads, const bws_kv_cache* cache,

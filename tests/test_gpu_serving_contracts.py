@@ -100,3 +100,23 @@ def test_attention_longer_than_its_table(m, D, H, K, n, past):
         sees = min(kv[0] - n + j + 1, held_tokens)
         check_rows(q[j:j + 1], c, t[:1], [0, 1], [sees], D ** -0.5, out[j:j + 1], lse[j:j + 1], slice(None))
     check_rows(q[n:], c, t[1:], [0, 1], [40], D ** -0.5, out[n:], lse[n:], slice(None))
+
+
+@pytest.mark.parametrize("D,H,K", [(64, 4, 2), (128, 8, 2), (256, 24, 4), (256, 16, 1)])
+def test_attention_more_rows_than_allowed(m, D, H, K):
+    """A request with more rows than max_rows: the first max_rows by their own sight, zeros for the rest, and a status."""
+    kv, rw, mx = [200, 90, 50], [2, 7, 1], 3
+    c, q, t, s, _ = attention_case(m, D, H, K, 16, rw, kv, seed=31)
+    ws = m.Workspace()
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device=device())
+    m.kv_attention(q, c, ints(t), ints(s), ints(kv), mx, out=out, lse=lse, ws=ws)
+    torch.cuda.synchronize()
+    live = np.ones(10, dtype=bool)
+    live[5:9] = False
+    check_rows(q, c, t, s, kv, D ** -0.5, out, lse, live)
+    assert (out[5:9] == 0).all() and (lse[5:9] == -float("inf")).all()
+    assert m.status_word(ws) == 0x10
+    m.kv_attention(q, c, ints(t), ints(s), ints(kv), 7, out=out, lse=lse, ws=ws)      # enough rows: none of it
+    torch.cuda.synchronize()
+    check_rows(q, c, t, s, kv, D ** -0.5, out, lse, slice(None))
+    assert m.status_word(ws) == 0
