@@ -206,11 +206,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
   pdl_launch_dependents();
   pdl_wait();
   const int start = min(max(p.row_start[r], 0), p.n_rows);
-  const int rows = min(max(p.row_start[r + 1] - start, 0), min(p.max_rows, p.n_rows - start));
-  if (rows == 0) {   // the whole cluster leaves
+  const int rows = max(min(p.row_start[r + 1], p.n_rows) - start, 0);
+  if (rows == 0 || rows > p.max_rows) {   // nothing to verify, or no room for it: the whole cluster leaves
     if (rank == 0) {
       for (int i = threadIdx.x; i < p.max_rows; i += kVerifyThreads) p.out[(size_t)r * p.max_rows + i] = -1;
-      if (threadIdx.x == 0) p.n_out[r] = 0;
+      if (threadIdx.x == 0) p.n_out[r] = rows == 0 ? 0 : -1;
     }
     cluster.barrier_wait();
     return;

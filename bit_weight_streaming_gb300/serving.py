@@ -229,11 +229,11 @@ def draft_verify(target, tokens, row_start, accept_u, sample_u, max_rows, draft=
     """Which drafted tokens stand against the target's probabilities, and the
     token drawn after them, from given uniform numbers. target fp32 [rows,
     vocab]; draft fp32 [rows, vocab] or None (each draft was certain), rows of
-    both at any stride of vocab or more; tokens
-    int32 [rows] (the last row of a request has no draft), accept_u fp32
-    [rows], row_start int32 [requests + 1], sample_u fp32 [requests]. Returns
-    (out int32 [requests, max_rows]: the drafts that stand, the drawn token,
-    then -1; n_out int32 [requests])."""
+    both at any stride of vocab or more; tokens int32 [rows] (the last row of
+    a request has no draft), accept_u fp32 [rows], row_start int32
+    [requests + 1], sample_u fp32 [requests]. Returns (out int32 [requests,
+    max_rows]: the drafts that stand, the drawn token, then -1; n_out int32
+    [requests], -1 for a request of more than max_rows rows)."""
     T, V = target.shape
     R = sample_u.shape[0]
     target_stride = _row_stride("target", target)

@@ -584,7 +584,8 @@ int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_str
  *   that stand, the drawn token, then -1; n_out int32 [n_requests] (0 for a
  *   request without rows). A token outside the vocabulary does not stand; a
  *   row without a positive weight draws -1.
- * 1 <= max_rows <= 32 bounds the rows of a request. One kernel. */
+ * 1 <= max_rows <= 32 bounds the rows of a request; one with more is not
+ * verified (n_out -1, out -1). One kernel. */
 int bws_draft_verify(const float* target, int64_t target_stride, const float* draft,
                      int64_t draft_stride, const int32_t* tokens, int n_rows, int vocab,
                      const int32_t* row_start, int n_requests, const float* accept_u,

@@ -157,6 +157,9 @@ def draft_verify(target, tokens, row_start, accept_u, sample_u, max_rows, draft=
         a, b = int(row_start[r]), int(row_start[r + 1])
         if b <= a:
             continue
+        if b - a > max_rows:
+            n_out[r] = -1
+            continue
         i = a
         while i < b - 1:
             x = int(tokens[i])

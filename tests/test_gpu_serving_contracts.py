@@ -120,3 +120,18 @@ def test_attention_more_rows_than_allowed(m, D, H, K):
     torch.cuda.synchronize()
     check_rows(q, c, t, s, kv, D ** -0.5, out, lse, slice(None))
     assert m.status_word(ws) == 0
+
+
+# ---- draft verification -------------------------------------------------------------------
+
+def test_verify_more_rows_than_allowed(m):
+    """A request with more rows than max_rows is refused on the device; its neighbours are not touched by it."""
+    p, q, tok, start, au, su = verify_case([2, 5, 3, 33], 1001, 36)
+    out, n = m.draft_verify(p, tok, ints(start), au, su, 3, draft=q)
+    torch.cuda.synchronize()
+    assert n.tolist()[1] == -1 and n.tolist()[3] == -1 and (out[1] == -1).all() and (out[3] == -1).all()
+    check_verify(m, p, q, tok, start, au, su, 3)
+    for r in (0, 2):
+        a, b = start[r], start[r + 1]
+        want, want_n = S.draft_verify(np_(p[a:b]), np_(tok[a:b]), [0, b - a], np_(au[a:b]), np_(su[r:r + 1]), 3, np_(q[a:b]))
+        assert n[r].item() == want_n[0] and np.array_equal(np_(out[r]), want[0])
