@@ -527,6 +527,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   pdl_wait();
   const int c = blockIdx.x;
   const uint32_t status = p.failed[0];   // what is said of the requests every CTA says
+  // rows of no request, as a captured step's padding: what reads them next finds zeros
+  clear_rows<D>(p, 0, min(p.row_start[0], p.n_rows));
+  clear_rows<D>(p, max(p.row_start[p.R], 0), p.n_rows);
   if (c == 0 && blockIdx.y == 0) {
     if (threadIdx.x == 0) s_bad = 0;
     __syncthreads();

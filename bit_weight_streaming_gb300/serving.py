@@ -4,6 +4,7 @@ the verification of drafted tokens (argument marshalling only; the contracts
 are in include/bws.h)."""
 import collections
 import ctypes as C
+import math
 
 import torch
 
@@ -194,7 +195,9 @@ def kv_attention(q, cache, block_table, row_start, kv_lens, max_rows, scale=None
     q_heads, dim], strided; block_table int32 [requests, max_blocks],
     row_start int32 [requests + 1], kv_lens int32 [requests]; scale defaults
     to dim ** -0.5. Returns out bf16 [rows, q_heads, dim], and with lse=True
-    also the fp32 [rows, q_heads] log-sum-exp of the scores."""
+    also the fp32 [rows, q_heads] log-sum-exp of the scores. Rows of no request
+    are zero (-inf), as are a request's past max_rows, which the workspace's
+    status word reports."""
     T, H, D = q.shape
     row, head = _check_heads("q", q, T, H, cache.head_dim)
     R, wide = block_table.shape
@@ -213,6 +216,11 @@ def kv_attention(q, cache, block_table, row_start, kv_lens, max_rows, scale=None
         else:
             _check("lse", lse, _F32, (T, H))
         lse_at = lse.data_ptr()
+    if R == 0:     # every row is one of no request
+        out.zero_()
+        if lse_at is not None:
+            lse.fill_(-math.inf)
+        return out if lse_at is None else (out, lse)
     so = lib()
     size = cache._attn_ws.get((H, max_rows))
     if size is None:

@@ -135,3 +135,29 @@ def test_verify_more_rows_than_allowed(m):
         a, b = start[r], start[r + 1]
         want, want_n = S.draft_verify(np_(p[a:b]), np_(tok[a:b]), [0, b - a], np_(au[a:b]), np_(su[r:r + 1]), 3, np_(q[a:b]))
         assert n[r].item() == want_n[0] and np.array_equal(np_(out[r]), want[0])
+
+
+@pytest.mark.parametrize("D,H,K,pad", [(64, 4, 2, 1), (128, 8, 2, 6), (256, 24, 4, 700)])
+def test_attention_rows_of_no_request(m, D, H, K, pad):
+    """Rows before the first request's and past the last one's, as the padding of a captured step, are zero."""
+    kv, rw = [200, 0, 50], [2, 0, 1]
+    c, q, t, s, mx = attention_case(m, D, H, K, 16, rw, kv, seed=32)
+    for before in (0, 2):
+        x = torch.full((before + 3 + pad, H, D), float("nan"), dtype=torch.bfloat16, device=device())
+        x[before:before + 3] = q
+        out, lse = torch.full_like(x, float("nan")), torch.full(x.shape[:2], float("nan"), device=device())
+        m.kv_attention(x, c, ints(t), ints(s + before), ints(kv), mx, out=out, lse=lse)
+        torch.cuda.synchronize()
+        mine = slice(before, before + 3)
+        check_rows(q, c, t, s, kv, D ** -0.5, out[mine], lse[mine], slice(None))
+        out[mine], lse[mine] = 0, -float("inf")
+        assert (out == 0).all() and (lse == -float("inf")).all()
+
+
+def test_attention_without_requests(m):
+    """No request at all: every row is one of no request."""
+    c, q, t, _, _ = attention_case(m, 64, 4, 2, 16, [3], [20], seed=33)
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device=device())
+    m.kv_attention(q, c, ints(t)[:0], ints([0]), ints([]), 3, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and (lse == -float("inf")).all()
