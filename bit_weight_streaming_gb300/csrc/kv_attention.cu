@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
   // ---- copies: 32 of the warp's units (first + warp, + 8, ...) at a time, a unit
   // a lane: the block (-1: not there) and the token in it.
   int mine, ids, toks;
-  auto token_of = [&](int i) { return (sg.first + warp + i * kAttnWarps) * kBox; };
+  auto token_of = [&](int i) { return (int)((uint32_t)(sg.first + warp + i * kAttnWarps) * kBox); };   // asked past the end too
   auto look_up = [&](int i, int& block, int& tok) {
     block = -1;
     tok = 0;

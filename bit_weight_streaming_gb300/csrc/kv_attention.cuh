@@ -71,7 +71,8 @@ BWS_DEV Request request_from(const AttnParams& p, int begin, int end, int kv, in
   q.seen0 = max(kv, 0) - rows;   // by the request's own length, where the table is too short for it as well
   const long long cap = (long long)p.max_blocks * p.B;
   q.kv = (int)min((long long)max(kv, 0), cap);
-  q.units = max(1, (q.kv + p.unit - 1) / p.unit);   // a request without tokens still writes its rows
+  // a request without tokens still writes its rows; unsigned, since kv may be all but 2^31
+  q.units = max(1, (int)((uint32_t)(q.kv + p.unit - 1u) / (uint32_t)p.unit));
   q.groups = (q.rows * p.G + group_rows - 1) / group_rows;
   return q;
 }

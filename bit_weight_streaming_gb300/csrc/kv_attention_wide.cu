@@ -197,8 +197,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     const Segment& sg = T.seg[turn];
     block = -1;
     tok = 0;
-    const int t = (sg.first + i) * kWideTile + b * kBox;
-    if (i < sg.last - sg.first && t < sg.rq.kv) {
+    // (unsigned: asked past the end too, and the last tile may end at 2^31)
+    const uint32_t t = (uint32_t)(sg.first + i) * kWideTile + b * kBox;
+    if (i < sg.last - sg.first && t < (uint32_t)sg.rq.kv) {
       const int q = block_index(p, t);
       const int id = p.table[(size_t)sg.r * p.max_blocks + q];
       tok = t - q * p.B;

@@ -161,3 +161,18 @@ def test_attention_without_requests(m):
     m.kv_attention(q, c, ints(t)[:0], ints([0]), ints([]), 3, out=out, lse=lse)
     torch.cuda.synchronize()
     assert (out == 0).all() and (lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("D,H,K,n", [(128, 2, 2, 1), (256, 24, 4, 8)])
+def test_attention_length_near_2_31(m, D, H, K, n):
+    """A table row of 2^31 - 16 tokens whose last blocks alone are there."""
+    B, wide = 16, 2 ** 27 - 1
+    tail = 109                                    # seven blocks but three tokens
+    kv = wide * B - 3
+    c, q, t, s, mx = attention_case(m, D, H, K, B, [n], [tail], seed=34)
+    last = -(-tail // B)
+    table = torch.full((1, wide), -1, dtype=torch.int32, device=device())
+    table[0, wide - last:] = ints(t[0, :last])
+    out, lse = m.kv_attention(q, c, table, ints([0, n]), ints([kv]), mx, lse=True)
+    torch.cuda.synchronize()
+    check_rows(q, c, t, s, [tail], D ** -0.5, out, lse, slice(None))
