@@ -32,6 +32,7 @@
 // code that is fetched anew.
 #include <atomic>
 
+#include "copy_ring.h"
 #include "kv_attention.cuh"
 
 namespace bws {
@@ -85,6 +86,7 @@ struct __align__(1024) WideTail {
   Walk walk;
   Segment seg[2];
   int more;
+  uint32_t started[kSoftWarps + kValueWarps];   // tiles whose box a warp has started to copy
   uint32_t tmem;
   uint32_t status;
 };
@@ -152,6 +154,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
                  "n"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (lane == 0) T.started[warp] = 0;
   if (tid == 0) {
     for (int s = 0; s < S::kKStages; ++s) mbar_init(k_full + 8 * s, kBoxes);
     for (int s = 0; s < S::kVStages; ++s) {
@@ -186,9 +189,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
   int turn = 0;
   // The (it / n)-th use of barrier it % n.
   auto wait_for = [&](uint32_t bars, uint32_t it, int n, bool freed) {
-    const uint32_t use = it / n;
-    if (freed && use == 0) return;   // nothing was there before
-    const uint32_t bar = bars + 8 * (it % n), parity = (freed ? use - 1 : use) & 1;
+    if (freed && it < (uint32_t)n) return;   // nothing was there before
+    const uint32_t bar = bars + 8 * ring_stage(it, n), parity = ring_parity(freed ? it - n : it, n);
     if (dead || __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
     dead = __any_sync(0xffffffffu, !mbar_wait_bounded(bar, parity, kAttnPolls));
   };
@@ -301,6 +303,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
       for (int i = 0; i < kMost; ++i)
         if (i < ahead)
           copy_box(my_bars, my_ring, keys ? &p.k : &p.v, (int)((phase_base + i) % my_stages), my_box, block[i], tok[i]);
+      T.started[warp] = phase_base + ahead;
     }
     __syncwarp();
   };
@@ -472,8 +475,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
         if (lane == 0) {
           mbar_arrive(p_full + 8 * buf);
           // the tile's products have read its keys: the next into their place
-          if (!dead && i + S::kKStages < tiles)
+          if (!dead && i + S::kKStages < tiles) {
             copy_box(k_full, k_ring, &p.k, (int)(it % S::kKStages), my_box, next_block, next_tok);
+            T.started[warp] = it + S::kKStages + 1;
+          }
           look_up(i + S::kKStages + 1, my_box, next_block, next_tok);
         }
         __syncwarp();
@@ -521,8 +526,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
         if (i > 0) {
           wait_for(v_free, it + S::kVStages - 1, S::kVStages, true);
           if (copies) {
-            if (!dead && i + S::kVStages - 1 < tiles)
+            if (!dead && i + S::kVStages - 1 < tiles) {
               copy_box(v_full, v_ring, &p.v, (int)((it + S::kVStages - 1) % S::kVStages), my_box, next_block, next_tok);
+              T.started[warp] = it + S::kVStages;
+            }
             look_up(i + S::kVStages, my_box, next_block, next_tok);
           }
           __syncwarp();
@@ -584,11 +591,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     }
     if (dead && lane == 0) {
       atomicOr(&T.status, (uint32_t)BWS_STATUS_WAIT_TIMEOUT);
-      // the copies still on their way
-      for (int s = 0; s < S::kKStages; ++s)
-        mbar_wait_bounded(k_full + 8 * s, (int)((phase_base / S::kKStages) & 1), kAttnPolls);
-      for (int s = 0; s < S::kVStages; ++s)
-        mbar_wait_bounded(v_full + 8 * s, (int)((phase_base / S::kVStages) & 1), kAttnPolls);
+      // this warp's copies still on their way; it starts no more
+      const uint32_t started = T.started[warp];
+      for (uint32_t it = ring_oldest(started, my_stages); it < started; ++it)
+        mbar_wait_bounded(my_bars + 8 * ring_stage(it, my_stages), ring_parity(it, my_stages), kAttnPolls);
+      T.started[warp] = 0;
     }
     phase_base += tiles;
     if (tid == 0) T.more = T.walk.next(p, S::kRows, T.seg[turn ^ 1]);

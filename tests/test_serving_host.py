@@ -120,6 +120,48 @@ def test_verify_refusals(lib):
     assert call(p=18) == 3 and call(n=17) == 3
 
 
+RING_MODEL = r"""
+#include <cstdio>
+#include "copy_ring.h"
+using namespace bws;
+// A barrier per stage counts the phases its landed uses completed; a wait on a parity passes when the phase of that
+// parity is the last one completed.
+int main() {
+  int bad = 0;
+  for (uint32_t n = 2; n <= 4; ++n)
+    for (uint32_t started = 1; started < 40; ++started)
+      for (uint32_t late = ring_oldest(started, n); late <= started; ++late) {   // the use that has not landed, if any
+        uint32_t phase[4] = {0, 0, 0, 0};
+        for (uint32_t it = 0; it < started; ++it)
+          if (it != late) ++phase[ring_stage(it, n)];
+        bool waited = false, seen[4] = {false, false, false, false};
+        for (uint32_t it = ring_oldest(started, n); it < started; ++it) {
+          const uint32_t s = ring_stage(it, n);
+          const bool passes = (phase[s] & 1u) != ring_parity(it, n);
+          bad += seen[s];                       // a stage is waited for once
+          seen[s] = true;
+          bad += passes != (it != late);        // what has landed passes, what has not is waited for
+          waited |= !passes;
+        }
+        bad += waited != (late < started);
+      }
+  std::printf("%d\n", bad);
+  return bad != 0;
+}
+"""
+
+
+def test_copies_on_their_way(tmp_path):
+    """A kernel that gives up a wait leaves only when its own copies have landed: it waits for the right phases."""
+    import os
+    import subprocess
+    src = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_weight_streaming_gb300", "csrc")
+    (tmp_path / "ring.cpp").write_text(RING_MODEL)
+    subprocess.run(["g++", "-std=c++17", "-I", src, "-o", str(tmp_path / "ring"), str(tmp_path / "ring.cpp")], check=True)
+    r = subprocess.run([str(tmp_path / "ring")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+
+
 def test_python_refuses_cpu_tensors():
     import torch
     import bit_weight_streaming_gb300 as bws
