@@ -9,9 +9,12 @@
 // largest). With a block's scales ks and vs,
 //   x = scale * log2(e) * ks * (q . code) + log2(vs),   w = 2^(x - m),
 //   out = sum w code_v / sum (w / vs),
-// m the running maximum of x: taking the value scale into the exponent keeps
-// every weight in [0, 1], whatever the blocks' scales, so that its rounding to
-// f16 (2^-11, finer than the BF16 result) is relative to the largest term.
+// m about the running maximum of x: taking the value scale into the exponent
+// keeps every weight within f16's reach (at most 2^15), whatever the blocks'
+// scales, and its rounding to f16 (2^-11 down to 2^-25 of the row's largest; finer
+// than the BF16 result) relative to the terms of the sum that it stands in. The
+// sum of weights takes them unrounded; a term leaves it only 2^135 below the
+// largest w.
 //
 // Work. A segment is one (request, kv head, group of 8 NT rows); its unit is 16
 // cached tokens (one TMA box a side; never across a block). All units of all
@@ -362,14 +365,13 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
           proxy_fence();   // before TMA writes the stage again
           __syncwarp();
         }
-        // ---- running maximum: m follows only where an exponent passes it by
-        // more than 8, so that most units compare and vote and no more (weights
-        // up to 2^8 cost f16 and FP32 nothing)
+        // ---- running maximum: m follows only past a margin, so that most units
+        // compare and vote and no more
         bool grew = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) grew |= x[n][k] > m[n][k & 1] + 8.0f;
+          for (int k = 0; k < 4; ++k) grew |= x[n][k] > m[n][k & 1] + kTop;
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
               float v = fmaxf(x[n][k], x[n][k + 2]);
 #pragma unroll
               for (int y = 4; y < 32; y <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, y));
-              const float to = fmaxf(m[n][k], v), f = exp2_fast(m[n][k] - to);
+              const float to = fmaxf(m[n][k], v - (kTop - kMargin)), f = exp2_fast(m[n][k] - to);
               m[n][k] = to;
               l[n][k] *= f;
 #pragma unroll

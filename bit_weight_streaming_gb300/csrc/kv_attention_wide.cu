@@ -22,9 +22,8 @@
 // issues the scores' products two tiles ahead, and each copies a box of keys and
 // values.
 // mbarriers with bounded waits join them; a wait that runs out marks the result
-// and goes on. One running maximum per row serves the CTA: it follows only where
-// an exponent passes it by more than 8, on which warps 0-7 vote, so most tiles
-// exchange no maxima.
+// and goes on. One running maximum per row serves the CTA: it follows only past a
+// margin, on which warps 0-7 vote, so most tiles exchange no maxima.
 // Bound: the chain of a tile, 4900 cycles at 48 rows of 256, of which the values'
 // mma.sync needs 3100 at 16 a quarter SM and HBM 2750: 100001 tokens of four kv
 // heads, 205 MB, take 68 us with the join (3.0 TB/s, 288 TFLOP/s). A segment costs
@@ -68,7 +67,7 @@ template <int D, int NT>
 struct __align__(1024) WideTail {
   uint8_t q[Wide<D, NT>::kPanels][Wide<D, NT>::kQPanel];      // swizzled as the keys are
   uint8_t p[2][kWideTile * Wide<D, NT>::kPStride];
-  alignas(16) float2 row[8 * NT];   // scale (with log2 e and the row's power of two), running maximum or 0
+  alignas(16) float2 row[8 * NT];   // scale (with log2 e and the row's power of two), what exponents are taken less, or 0
   uint32_t fresh[2];           // bit r: row r has seen no token yet, and its maximum stands for nothing
   float up[8 * NT];            // how far the maxima went in a tile that moved them
   float top[kQuads][8 * NT];
@@ -367,7 +366,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
         fence_after();
         const uint32_t s_at = tmem + buf * 128 + ((uint32_t)(32 * quad) << 16) + row_a;
         const float2* const rows = T.row + row_a;
-        // exponents of every row, less the running maximum
+        // exponents of every row, less what stands for its maximum
         float x[kHalf];
         float top = -INFINITY;
         uint32_t hi[kHalf], lo[kHalf];
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
         }
 #pragma unroll
         for (int n = 0; n < kHalf; ++n) top = fmaxf(top, x[n]);
-        const bool grew = top > 8.0f || ((T.fresh[0] | T.fresh[1]) != 0u && top != -INFINITY);
+        const bool grew = top > kTop || ((T.fresh[0] | T.fresh[1]) != 0u && top != -INFINITY);
         uint32_t any;
         asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, %2, %3, p; selp.u32 %0, 1, 0, q; }"
                      : "=r"(any) : "r"((uint32_t)grew), "n"(kBarSoft), "n"(32 * kSoftWarps) : "memory");
@@ -405,7 +404,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
             const bool row = tid < S::kRows, fresh = row && ((T.fresh[warp] >> lane) & 1u) != 0u;
             float up = -INFINITY;
             if (row)
-              for (int w = 0; w < kQuads; ++w) up = fmaxf(up, T.top[w][tid]);
+              for (int w = 0; w < kQuads; ++w) up = fmaxf(up, T.top[w][tid] - (kTop - kWideMargin));
             const bool still = fresh && up == -INFINITY;
             if (!fresh || still) up = fmaxf(up, 0.0f);
             if (row) {

@@ -547,7 +547,11 @@ int bws_qk_norm_rope_append(const bws_qkv* in, const bws_kv_cache* cache,
  * row_start[r+1] - row_start[r] rows (so the rows are the request's last
  * tokens, already in the cache). Query head h reads kv head h / (n_q_heads /
  * n_kv_heads). A row that sees no token gives 0 (lse -inf). Codes are exact in
- * the products; sums and softmax statistics are FP32. Table entries outside
+ * the products; sums and softmax statistics are FP32. A weight (times its
+ * block's value scale) is rounded to f16 for the values' product: by 2^-11
+ * down to 2^-23 of the row's largest, by at most 2^-34 of that largest below.
+ * Of more than 16 rows of 256 or 32 of 128 a kv head, a query value below
+ * 2^-14 of its row's largest is off by up to 2^-22 of that. Table entries outside
  * the cache, and tokens past the table row, count as tokens that are not there.
  *   q bf16 [n_rows][n_q_heads][head_dim], innermost contiguous, strides in
  *   elements (multiples of 8), 16-byte aligned; block_table int32 [n_requests]

@@ -176,3 +176,64 @@ def test_attention_length_near_2_31(m, D, H, K, n):
     out, lse = m.kv_attention(q, c, table, ints([0, n]), ints([kv]), mx, lse=True)
     torch.cuda.synchronize()
     check_rows(q, c, t, s, [tail], D ** -0.5, out, lse, slice(None))
+
+
+def attend64(q, c, kv, scale):
+    """One request over blocks 0, 1, ... in FP64: output, log-sum-exp, sum p |v|, the largest score's absolute sum."""
+    n, H, D = q.shape
+    K = c.kv_heads
+    side = lambda s: c.dequantize(s).transpose(0, 1).reshape(K, -1, D)[:, :kv].double()  # noqa: E731
+    k, v = side("k"), side("v")
+    x = q.double().view(n, K, H // K, D).permute(1, 0, 2, 3)                     # [K, n, G, D]
+    hide = torch.arange(kv, device=q.device) > (kv - n + torch.arange(n, device=q.device))[:, None]
+    z = (torch.einsum("kngd,ktd->kngt", x, k) * scale).masked_fill(hide[None, :, None], -float("inf"))
+    score = (torch.einsum("kngd,ktd->kngt", x.abs(), k.abs()) * scale).masked_fill(hide[None, :, None], 0).amax(-1)
+    lse = torch.logsumexp(z, -1)
+    p = torch.exp(z - lse[..., None])
+    back = lambda t: t.permute(1, 0, 2, *range(3, t.dim())).reshape(n, H, *t.shape[3:]).cpu().numpy()  # noqa: E731
+    return (back(torch.einsum("kngt,ktd->kngd", p, v)), back(lse), back(torch.einsum("kngt,ktd->kngd", p, v.abs())),
+            back(score))
+
+
+SINK_FORMS = [(64, 16, 4, 1), (64, 16, 4, 8), (128, 8, 4, 1), (128, 16, 4, 3), (256, 24, 4, 1), (256, 24, 4, 8), (256, 16, 1, 8),
+              (128, 32, 2, 8), (256, 16, 1, 2)]
+
+
+def sink_case(m, D, H, K, n, kv, gap, where):
+    """Tokens whose scores differ by half a nat and carry values about 1, behind one that lies `gap` nats above them and
+    carries none."""
+    B, g = 64, gen(gap + D)
+    n_blocks = -(-kv // B)
+    k = torch.randn((n_blocks, K, B, D), generator=g, device=device())
+    v = 1 + 0.25 * torch.randn((n_blocks, K, B, D), generator=g, device=device())
+    k[..., 0] = 0
+    k[where // B, :, where % B] = 0
+    v[where // B, :, where % B] = 0
+    code = min(gap, 16)                       # E4M3 has no 17
+    k[where // B, :, where % B, 0] = code
+    e4 = lambda x: x.to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+    s = torch.ones((2, n_blocks, K), device=device())
+    c = m.KvCache(e4(k), e4(v), s[0], s[1])
+    q = 0.5 * D ** -0.5 * torch.randn((n, H, D), generator=g, device=device())
+    q[..., 0] = gap / code
+    return c, q.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("gap", [12, 13, 14, 15, 16, 17])
+@pytest.mark.parametrize("D,H,K,n", SINK_FORMS)
+def test_attention_dominant_token(m, D, H, K, n, gap):
+    """A token that takes most of the weight and carries no value leaves the others their precision: whole segments (many
+    requests over the same blocks) and one that is cut."""
+    kv = 9001
+    c, q = sink_case(m, D, H, K, n, kv, gap, 3)
+    want = attend64(q, c, kv, 1.0)
+    t = [list(range(c.n_blocks))]
+    R = 320 // K
+    out, lse = m.kv_attention(q.repeat(R, 1, 1), c, ints(t * R), ints([n * r for r in range(R + 1)]), ints([kv] * R), n, 1.0,
+                              lse=True)
+    torch.cuda.synchronize()
+    for r in (0, 1, R // 2, R - 1):
+        check_result(f64(out[r * n:(r + 1) * n]), f64(lse[r * n:(r + 1) * n]), *want, D)
+    out, lse = m.kv_attention(q, c, ints(t), ints([0, n]), ints([kv]), n, 1.0, lse=True)
+    torch.cuda.synchronize()
+    check_result(f64(out), f64(lse), *want, D)
