@@ -11,7 +11,7 @@
 //   out = sum w code_v / sum (w / vs),
 // m about the running maximum of x: taking the value scale into the exponent
 // keeps every weight within f16's reach (at most 2^15), whatever the blocks'
-// scales, and its rounding to f16 (2^-11 down to 2^-25 of the row's largest; finer
+// scales, and its rounding to f16 (2^-11 down to 2^-23 of the row's largest; finer
 // than the BF16 result) relative to the terms of the sum that it stands in. The
 // sum of weights takes them unrounded; a term leaves it only 2^135 below the
 // largest w.
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     block = -1;
     tok = 0;
     const int t = token_of(i);
-    if (i < mine && t < sg.rq.kv) {
+    if (i < mine && t < sg.rq.kv(p)) {
       const int q = block_index(p, t);
       const int b = p.table[(size_t)sg.r * p.max_blocks + q];
       tok = t - q * p.B;
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
   auto ask_segment = [&]() {
     mine = (sg.last - sg.first - warp + kAttnWarps - 1) / kAttnWarps;
     look_up(lane, ids, toks);
-    const int n_rows = min(sg.rq.rows * p.G - sg.row0, S::kRows);
+    const int n_rows = min(sg.rq.rows(p) * p.G - sg.row0, S::kRows);
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
       const int n = warp + k * kAttnWarps;
@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     const Segment cur = sg;
     const Request& rq = cur.rq;
     const int row0 = cur.row0, head = cur.head;
-    const int n_group_rows = min(rq.rows * p.G - row0, S::kRows);
-    const int seen0 = rq.seen0;   // row j sees tokens <= seen0 + j
+    const int n_group_rows = min(rq.rows(p) * p.G - row0, S::kRows);
+    const int seen0 = rq.seen0();   // row j sees tokens <= seen0 + j
     uint32_t* const nan_mask = T.nan_mask[turn];
 
     uint32_t qf[S::kQInRegs ? kMT : 1][S::kQInRegs ? NT : 1][2];
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const int lim = min(seen0 + (row0 + n * 8 + t4 * 2 + k) / p.G, rq.kv - 1);
+              const int lim = min(seen0 + (row0 + n * 8 + t4 * 2 + k) / p.G, rq.len - 1);
               if (tok0 + g > lim) x[n][k] = -INFINITY;
               if (tok0 + g + 8 > lim) x[n][k + 2] = -INFINITY;
             }
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
             const uint32_t at = vs_at + chunk_at<D>(tk, byte >> 4) + (byte & 15);
             uint32_t word;
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(word) : "r"(at) : "memory");
-            if (tok0 + tk >= rq.kv) {
+            if (tok0 + tk >= rq.len) {   // (a table row ends with a box)
               word = 0;
             } else {
 #pragma unroll
@@ -501,16 +501,25 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
   if (tid == 0) p.failed[cta] = T.status;
 }
 
-// Rows [from, to) of the output become what a row without tokens is; the CTAs
-// of the grid take them in turn.
+// Output rows without a result of their own become what a row without tokens is:
+// rows of no request (before `begin`, from `end` on), as a captured step's padding,
+// and a request's rows past max_rows. The first row's CTAs take them in turn. Out of
+// line: the join lasts a few loads, and a call without such rows fetches none of it.
 template <int D>
-BWS_DEV void clear_rows(const AttnParams& p, int from, int to) {
-  const int n = gridDim.x * gridDim.y;
-  for (int row = from + blockIdx.y * gridDim.x + blockIdx.x; row < to; row += n) {
-    uint4* const out = reinterpret_cast<uint4*>(p.out + (size_t)row * p.H * D);
-    for (int i = threadIdx.x; i < p.H * (D / 8); i += blockDim.x) out[i] = make_uint4(0, 0, 0, 0);
-    if (p.lse != nullptr)
-      for (int i = threadIdx.x; i < p.H; i += blockDim.x) p.lse[(size_t)row * p.H + i] = -INFINITY;
+__device__ __noinline__ void clear_rows(const AttnParams& p, int begin, int end, bool excess) {
+  auto clear = [&](int from, int to) {
+    for (int row = from + blockIdx.x; row < to; row += gridDim.x) {
+      uint4* const out = reinterpret_cast<uint4*>(p.out + (size_t)row * p.H * D);
+      for (int i = threadIdx.x; i < p.H * (D / 8); i += blockDim.x) out[i] = make_uint4(0, 0, 0, 0);
+      if (p.lse != nullptr)
+        for (int i = threadIdx.x; i < p.H; i += blockDim.x) p.lse[(size_t)row * p.H + i] = -INFINITY;
+    }
+  };
+  clear(0, min(begin, p.n_rows));
+  clear(max(end, 0), p.n_rows);
+  for (int r = 0; excess && r < p.R; ++r) {
+    const Request q = request_of(p, r, p.group_rows);
+    clear(q.start + q.rows(p), q.start + q.all);
   }
 }
 
@@ -528,28 +537,23 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   pdl_launch_dependents();
   pdl_wait();
   const int c = blockIdx.x;
-  const uint32_t status = p.failed[0];   // what is said of the requests every CTA says
-  // rows of no request, as a captured step's padding: what reads them next finds zeros
-  clear_rows<D>(p, 0, min(p.row_start[0], p.n_rows));
-  clear_rows<D>(p, max(p.row_start[p.R], 0), p.n_rows);
-  if (c == 0 && blockIdx.y == 0) {
-    if (threadIdx.x == 0) s_bad = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.n_ctas; i += 256)
-      if (p.failed[i] != 0) atomicOr(&s_bad, p.failed[i]);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      p.hdr[0] = 0;
-      p.hdr[1] = s_bad;
+  const int4 cut = p.cut[2 * c], more = p.cut[2 * c + 1];
+  if (blockIdx.y == 0) {
+    const int begin = p.row_start[0], end = p.row_start[p.R];
+    const bool excess = (p.failed[0] & BWS_STATUS_KV_ROWS) != 0u;   // every CTA says it
+    if (c == 0) {
+      if (threadIdx.x == 0) s_bad = 0;
+      __syncthreads();
+      for (int i = threadIdx.x; i < p.n_ctas; i += 256)
+        if (p.failed[i] != 0) atomicOr(&s_bad, p.failed[i]);
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        p.hdr[0] = 0;
+        p.hdr[1] = s_bad;
+      }
     }
+    if (begin > 0 || end < p.n_rows || excess) clear_rows<D>(p, begin, end, excess);
   }
-  if (status & BWS_STATUS_KV_ROWS)
-    for (int r = 0; r < p.R; ++r) {
-      const Request q = request_of(p, r, kRows);
-      clear_rows<D>(p, q.start + q.rows, q.start + q.rows + q.excess);
-    }
-  const int4 cut = p.cut[2 * c];
-  const int4 more = p.cut[2 * c + 1];
   if (p.by_segment) {   // a request's missing row groups have no entry
     const int r = c / (p.K * p.max_groups);
     if (c % p.max_groups >= request_of(p, r, kRows).groups) return;
@@ -561,7 +565,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   auto slot_of = [&](int i) { return (first + i) * 2 + (i == 0 ? 1 : 0); };
   const int d4 = threadIdx.x % kLanes, at = threadIdx.x / kLanes;
   float top = kNone;
-  for (int i = 0; i < pieces; ++i) top = fmaxf(top, p.part_ml[(size_t)slot_of(i) * kRows + n].x);
+  // a piece a lane: asked for one after the other by every thread they are a fifth of the join's time at 38 pieces
+  for (int i = threadIdx.x & 31; i < pieces; i += 32) top = fmaxf(top, p.part_ml[(size_t)slot_of(i) * kRows + n].x);
+  top = warp_max(top);
   float4 a = make_float4(0, 0, 0, 0);
   float l = 0.0f;
 #pragma unroll 4
@@ -764,6 +770,7 @@ int bws_kv_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_str
   p.v_scale = cache->v_scale;
   p.table = block_table;
   p.max_blocks = max_blocks;
+  p.max_tokens = max_blocks * cache->block_tokens;
   p.R = n_requests;
   p.row_start = row_start;
   p.kv_lens = kv_lens;

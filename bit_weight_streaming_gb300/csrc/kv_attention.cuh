@@ -22,12 +22,10 @@ constexpr float kNone = -3.0e38f;           // a running maximum of nothing
 // rounded by 2^-11 down to 2^-(kTop - margin + 14) of a row's largest; below that
 // f16's step is fixed. That tail counts: a token that takes most of the weight and
 // carries no value leaves the result to all the others. A smaller margin reaches
-// further down and moves the maxima more often. Four octaves cost the kernel for
-// few rows nothing against eight (24x5 37.9 us, 80x1 123.6); in the wide one, where
-// the warps meet for it, 8 rows at 100001 take 71.6 us with a margin of 8, 72 with
-// 7, 73 with 6, 74.7 with 5, 77 with 4.
-constexpr float kTop = 15.0f;
-constexpr float kMargin = 4.0f, kWideMargin = 6.0f;
+// further down and moves the maxima more often. With a margin of 4 / 6 / 8, us: 8
+// rows of 24 heads at 100001 (256) 71 / 67.8 / 66.8, 8 of 64 (64, 100001) 92.4 / 88.8
+// / 87.7, 24 requests of 8 rows (256, short) - / 35.6 / 34.7, 80 of one row alike.
+constexpr float kTop = 15.0f, kMargin = 6.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -41,6 +39,7 @@ struct AttnParams {
   const float *k_scale, *v_scale;
   const int32_t* table;
   int max_blocks, R;
+  int max_tokens;     // of a table row
   const int32_t *row_start, *kv_lens;
   int max_rows;
   float scale;
@@ -68,23 +67,22 @@ BWS_DEV int block_index(const AttnParams& p, int token) {
 }
 
 struct Request {
-  int rows, start, kv, units, groups;   // kv: tokens that the table row can hold; units of one segment; row groups
-  int seen0;                            // the last token that row 0 sees; row j sees j more
-  int excess;                           // rows beyond max_rows
+  int start, all, len;    // its first row; its rows, of which max_rows are computed; its tokens, by the caller's word
+  int units, groups;      // units of one segment; row groups
+  // What follows from these is formed where it is used: kept beside them it cost registers that the loops need.
+  BWS_DEV int rows(const AttnParams& p) const { return min(all, p.max_rows); }
+  BWS_DEV int kv(const AttnParams& p) const { return min(len, p.max_tokens); }   // tokens that the table row can hold
+  BWS_DEV int seen0() const { return len - all; }   // the last token that row 0 sees; row j sees j more
 };
 
 BWS_DEV Request request_from(const AttnParams& p, int begin, int end, int kv, int group_rows) {
   Request q;
   q.start = min(max(begin, 0), p.n_rows);
-  const int rows = max(min(end, p.n_rows) - q.start, 0);
-  q.rows = min(rows, p.max_rows);
-  q.excess = rows - q.rows;
-  q.seen0 = max(kv, 0) - rows;   // by the request's own length, where the table is too short for it as well
-  const long long cap = (long long)p.max_blocks * p.B;
-  q.kv = (int)min((long long)max(kv, 0), cap);
+  q.all = max(min(end, p.n_rows) - q.start, 0);
+  q.len = max(kv, 0);
   // a request without tokens still writes its rows; unsigned, since kv may be all but 2^31
-  q.units = max(1, (int)((uint32_t)(q.kv + p.unit - 1u) / (uint32_t)p.unit));
-  q.groups = (q.rows * p.G + group_rows - 1) / group_rows;
+  q.units = max(1, (int)((uint32_t)(q.kv(p) + p.unit - 1u) / (uint32_t)p.unit));
+  q.groups = (q.rows(p) * p.G + group_rows - 1) / group_rows;
   return q;
 }
 
@@ -115,7 +113,7 @@ BWS_DEV Line find_on_line(const AttnParams& p, int group_rows, int cta, long lon
   for (int r = r0; r < r1; ++r) {
     const Request q = request_of(p, r, group_rows);
     mine += length_of(p, q);
-    excess |= q.excess > 0;
+    excess |= q.all > p.max_rows;
   }
   long long inc = mine;
 #pragma unroll
@@ -228,7 +226,7 @@ struct Walk {
       sg.pieces = sg.starts && !sg.whole ? (int)((b - 1) / share) - cta + 1 : 1;
       if (sg.starts && threadIdx.x == 0 && (sg.pieces > 1 || p.by_segment)) {   // for the join
         const int c = p.by_segment ? (r * p.K + sg.head) * p.max_groups + s - sg.head * rq.groups : cta;
-        p.cut[2 * c] = make_int4(rq.start, min(rq.rows * p.G - sg.row0, group_rows), sg.head, sg.row0);
+        p.cut[2 * c] = make_int4(rq.start, min(rq.rows(p) * p.G - sg.row0, group_rows), sg.head, sg.row0);
         p.cut[2 * c + 1] = make_int4(sg.pieces, cta, 0, 0);
       }
       return true;

@@ -188,8 +188,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
   int turn = 0;
   // The (it / n)-th use of barrier it % n.
   auto wait_for = [&](uint32_t bars, uint32_t it, int n, bool freed) {
-    if (freed && it < (uint32_t)n) return;   // nothing was there before
-    const uint32_t bar = bars + 8 * ring_stage(it, n), parity = ring_parity(freed ? it - n : it, n);
+    const uint32_t use = it / n;
+    if (freed && use == 0) return;   // nothing was there before
+    const uint32_t bar = bars + 8 * (it % n), parity = (freed ? use - 1 : use) & 1;
     if (dead || __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
     dead = __any_sync(0xffffffffu, !mbar_wait_bounded(bar, parity, kAttnPolls));
   };
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     tok = 0;
     // (unsigned: asked past the end too, and the last tile may end at 2^31)
     const uint32_t t = (uint32_t)(sg.first + i) * kWideTile + b * kBox;
-    if (i < sg.last - sg.first && t < (uint32_t)sg.rq.kv) {
+    if (i < sg.last - sg.first && t < (uint32_t)sg.rq.kv(p)) {
       const int q = block_index(p, t);
       const int id = p.table[(size_t)sg.r * p.max_blocks + q];
       tok = t - q * p.B;
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
   auto store_queries = [&]() {
     constexpr int E = D / 32;   // neighbouring values a lane
     const Segment& sg = T.seg[turn];
-    const int n_rows = min(sg.rq.rows * p.G - sg.row0, S::kRows);
+    const int n_rows = min(sg.rq.rows(p) * p.G - sg.row0, S::kRows);
     // Every row is asked for before the first is used; lane r knows where the r-th
     // lies. The rows are then converted by one rolled loop, whose instructions
     // are fetched once.
@@ -317,7 +318,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     const Segment& cur = T.seg[turn];
     const Request& rq = cur.rq;
     const int tiles = cur.last - cur.first;
-    const int seen0 = rq.seen0;          // row j sees tokens <= seen0 + j
     uint32_t* const nan_mask = T.nan_mask[turn];
     float o[S::kMT][NT][4];              // the value warps'
     const int g = lane >> 2, t4 = lane & 3;
@@ -356,8 +356,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
         scales_of(block_n, ks_n, vs_n);
         block_n = block_of(i + 2);
         const float lvs = log2f(vs), rvs = 1.0f / vs;
-        const int tok = (cur.first + i) * kWideTile + token, own = min(tok - seen0, 31);
-        const bool there = ks != -1.0f && tok < rq.kv;
+        const int tok = (cur.first + i) * kWideTile + token, own = min(tok - rq.seen0(), 31);   // row j sees tokens <= seen0 + j
+        const bool there = ks != -1.0f && tok < rq.kv(p);
         // rows below `hidden` do not see the token: the j-th token of the rows'
         // own is seen from row j on
         const int hidden = !there ? S::kRows : own > 0 ? min(max(own * p.G - cur.row0, 0), S::kRows) : 0;
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
             const bool row = tid < S::kRows, fresh = row && ((T.fresh[warp] >> lane) & 1u) != 0u;
             float up = -INFINITY;
             if (row)
-              for (int w = 0; w < kQuads; ++w) up = fmaxf(up, T.top[w][tid] - (kTop - kWideMargin));
+              for (int w = 0; w < kQuads; ++w) up = fmaxf(up, T.top[w][tid] - (kTop - kMargin));
             const bool still = fresh && up == -INFINITY;
             if (!fresh || still) up = fmaxf(up, 0.0f);
             if (row) {
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
           while (todo != 0u) {
             const int tk = __ffs(todo) - 1;
             todo &= todo - 1;
-            const int its = (cur.first + i) * kWideTile + quad * 32 + tk - seen0;
+            const int its = (cur.first + i) * kWideTile + quad * 32 + tk - rq.seen0();
 #pragma unroll
             for (int byte = 4 * lane; byte < D; byte += 128) {
               const uint32_t at = side + tile_chunk_at(quad * 32 + tk, byte >> 4) + (byte & 15);
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     if (warp < kSoftWarps) {
       if (more) store_queries();
     } else {
-      const int vw = warp - kSoftWarps, row0 = cur.row0, n_group_rows = min(rq.rows * p.G - row0, S::kRows);
+      const int vw = warp - kSoftWarps, row0 = cur.row0, n_group_rows = min(rq.rows(p) * p.G - row0, S::kRows);
       const int slot = blockIdx.x * 2 + (cur.starts ? 1 : 0);
       const bool whole = cur.whole;
       // A row's place, factor and sight are formed by a lane of their own and
