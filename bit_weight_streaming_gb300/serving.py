@@ -52,7 +52,8 @@ def _check_heads(name, t, rows, heads, dim):
     row, head, one = t.stride()
     if one != 1:
         raise BwsError(f"{name} must be contiguous in its last dimension")
-    return row, head
+    # a dimension of one entry has no stride of its own
+    return row if rows > 1 else 0, head if heads > 1 else 0
 
 
 def _row_stride(name, t):

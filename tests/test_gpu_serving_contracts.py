@@ -237,3 +237,23 @@ def test_attention_dominant_token(m, D, H, K, n, gap):
     out, lse = m.kv_attention(q, c, ints(t), ints([0, n]), ints([kv]), n, 1.0, lse=True)
     torch.cuda.synchronize()
     check_result(f64(out), f64(lse), *want, D)
+
+
+# ---- arguments -------------------------------------------------------------------------
+
+def test_single_row_and_head_strides(m):
+    """A dimension of one entry has no stride of its own: whatever stands there is not looked at."""
+    D, B = 64, 16
+    g = gen(35)
+    c = make_cache(m, 4, 1, B, D)
+    flat = rows(1, 1, 8 * D, g).view(-1)
+    q = flat.as_strided((1, 4, D), (4 * D + 3, D, 1))
+    k = flat[4 * D:].as_strided((1, 1, D), (D + 1, 5, 1))
+    v = flat[5 * D:].as_strided((1, 1, D), (1, 1, 1))
+    w = torch.ones(D, device=device())
+    state = held(c)
+    check_append(m, c, state, q, k, v, [0], [16], freqs(D), w, w)
+    a = m.kv_attention(q, c, ints([[1]]), ints([0, 1]), ints([1]), 1)
+    b = m.kv_attention(q.contiguous(), c, ints([[1]]), ints([0, 1]), ints([1]), 1)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
