@@ -227,6 +227,8 @@ def kv_attention(q, cache, block_table, row_start, kv_lens, max_rows, scale=None
     if size is None:
         size = cache._attn_ws[H, max_rows] = kv_attention_workspace_size(H, cache.kv_heads, D, max_rows)
     buf = _ws(ws, size, q.device)
+    if not buf.is_cuda or buf.dtype is not _U8:
+        raise BwsError(f"the workspace must be CUDA uint8 memory; it is {buf.dtype} on {buf.device}")
     _fail(so.bws_kv_attention(q.data_ptr(), row, head, T, H, cache._at, block_table.data_ptr(), wide, R,
                               row_start.data_ptr(), kv_lens.data_ptr(), max_rows, D ** -0.5 if scale is None else scale,
                               out.data_ptr(), lse_at, buf.data_ptr(), buf.numel(), _raw_stream(q.get_device())),

@@ -241,6 +241,13 @@ def test_attention_dominant_token(m, D, H, K, n, gap):
 
 # ---- arguments -------------------------------------------------------------------------
 
+def test_attention_refuses_host_workspace(m):
+    c, q, t, s, n = attention_case(m, 64, 4, 2, 16, [1], [20], seed=37)
+    for ws in (m.Workspace("cpu"), torch.zeros(1 << 24, dtype=torch.uint8), torch.zeros(1 << 24, device=device())):
+        with pytest.raises(m.BwsError, match="workspace"):
+            m.kv_attention(q, c, ints(t), ints(s), ints([20]), n, ws=ws)
+
+
 def test_single_row_and_head_strides(m):
     """A dimension of one entry has no stride of its own: whatever stands there is not looked at."""
     D, B = 64, 16
