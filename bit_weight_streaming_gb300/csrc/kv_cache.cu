@@ -629,7 +629,8 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_
         form(row_at(row + i), pos_at(row + i), x);
         if (i < m) store_codes(dst + (size_t)i * D, x, inv);
       }
-      if (!solo) __syncthreads();   // every thread has read the old scale and s_amax
+      if (solo) __syncwarp();   // every thread has read the old scale, and s_amax
+      else __syncthreads();
       if (solo ? lane == 0 : threadIdx.x == 0) *scale_at = scale;
     }
   }
