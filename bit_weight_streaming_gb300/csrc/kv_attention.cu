@@ -659,19 +659,9 @@ bool attn_dims_ok(int H, int K, int D, int max_rows) {
 template <int D, int NT>
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> attr{0};
-  cudaError_t e = set_smem_once(attr, attn_kernel<D, NT>, attn_smem<D, NT>());
+  const cudaError_t e = set_smem_once(attr, attn_kernel<D, NT>, attn_smem<D, NT>());
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.n_ctas);
-  cfg.blockDim = dim3(kAttnThreads);
-  cfg.dynamicSmemBytes = attn_smem<D, NT>();
-  cfg.stream = st;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_kernel<D, NT>, p);
+  return launch_pdl(attn_kernel<D, NT>, dim3((unsigned)p.n_ctas), kAttnThreads, attn_smem<D, NT>(), st, p);
 }
 
 template <int D>
@@ -687,18 +677,10 @@ cudaError_t launch_attn_d(Form form, const AttnParams& p, cudaStream_t st) {
     if (!form.wide && form.nt == 8) e = launch_attn<D, 8>(p, st);
   }
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
   const int rows = p.max_rows * p.G;
-  cfg.gridDim = dim3((unsigned)(p.by_segment ? p.R * p.K * p.max_groups : p.n_ctas),
-                     (unsigned)(rows < p.group_rows ? rows : p.group_rows));
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
+  const dim3 grid((unsigned)(p.by_segment ? p.R * p.K * p.max_groups : p.n_ctas),
+                  (unsigned)(rows < p.group_rows ? rows : p.group_rows));
+  return launch_pdl(join_kernel<D>, grid, 256, 0, st, p);
 }
 
 }  // namespace

@@ -33,6 +33,7 @@
 
 #include "copy_ring.h"
 #include "kv_attention.cuh"
+#include "kv_cache.cuh"
 
 namespace bws {
 namespace {
@@ -688,17 +689,7 @@ cudaError_t launch_wide(const AttnParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> attr{0};
   const cudaError_t e = set_smem_once(attr, attn_wide_kernel<D, NT>, wide_smem<D, NT>());
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.n_ctas);
-  cfg.blockDim = dim3(kWideThreads);
-  cfg.dynamicSmemBytes = wide_smem<D, NT>();
-  cfg.stream = st;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_wide_kernel<D, NT>, p);
+  return launch_pdl(attn_wide_kernel<D, NT>, dim3((unsigned)p.n_ctas), kWideThreads, wide_smem<D, NT>(), st, p);
 }
 
 }  // namespace

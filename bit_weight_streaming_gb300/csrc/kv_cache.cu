@@ -517,15 +517,6 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_
   // The runs that start in the span, in order. Where the CTA shares it, every
   // warp finds them all; a short one is a warp's alone, with no barrier; a long
   // one is the whole CTA's.
-  auto largest = [&](const float (&x)[8], float amax) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float a = fabsf(x[k]);
-      if (a < INFINITY) amax = fmaxf(amax, a);   // NaN and infinity set no scale
-    }
-    return amax;
-  };
-
   int turn = 0;   // short runs so far
   for (int t = t0; t < t1; t += 31) {
     // rows t - 1 .. t + 30's slots, a lane each
@@ -636,26 +627,11 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_
   }
 }
 
-template <typename K, typename P>
-cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t st, const P& p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 template <int D>
 cudaError_t launch_append(unsigned grid, size_t smem, cudaStream_t st, const AppendParams& p) {
   static std::atomic<unsigned long long> attr{0};
   const cudaError_t e = set_smem_once(attr, append_kernel<D>, kAppendWarps * 10 * 256 * 4);
-  return e != cudaSuccess ? e : launch_pdl(append_kernel<D>, grid, kAppendThreads, smem, st, p);
+  return e != cudaSuccess ? e : launch_pdl(append_kernel<D>, dim3(grid), kAppendThreads, smem, st, p);
 }
 
 }  // namespace
@@ -732,7 +708,7 @@ int bws_kv_plan_bounded(const int32_t* seq_lens, const int32_t* new_lens, int n_
   const long long want = ((long long)n_rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
   const long long most = 2LL * num_sms();
   const unsigned grid = (unsigned)(want < 1 ? 1 : want > most ? most : want);
-  return cuda_status(launch_pdl(plan_kernel, grid, kPlanThreads, sizeof(int) * (3 * (size_t)n_requests + 2),
+  return cuda_status(launch_pdl(plan_kernel, dim3(grid), kPlanThreads, sizeof(int) * (3 * (size_t)n_requests + 2),
                                 as_stream(stream), p), name);
 }
 
