@@ -65,6 +65,26 @@ def test_plan_takes_only_what_tables_hold(m, seq, new, wide, n_free):
     assert p.status.item() & 2 and bool(p.status.item() & 1) == (wanted > n_free)
 
 
+# ---- norm, rotation, cache write ---------------------------------------------------
+
+@pytest.mark.parametrize("D,rot,inter", [(64, 48, False), (64, 48, True), (128, 96, False), (128, 80, True), (256, 192, False),
+                                         (256, 144, False), (256, 160, True), (256, 128, False)])
+def test_append_more_than_half_rotated(m, D, rot, inter):
+    """Most of a head turns but not all of it: short runs, long runs, a prompt of many spans."""
+    H, K, B = 3, 2, 32
+    g = gen(D + rot)
+    w = [1 + 0.2 * torch.randn(D, generator=g, device=device()) for _ in range(2)]
+    cache = make_cache(m, 70, K, B, D)
+    state = held(cache)
+    at = 0
+    for n in (1, 5, 70, 2000):
+        pos = list(range(at, at + n))
+        slots = [(p // B * 7 % 67) * B + p % B for p in pos]
+        state = check_append(m, cache, state, rows(n, H, D, g), rows(n, K, D, g), rows(n, K, D, g), pos, slots, freqs(rot),
+                             w[0], w[1], inter)
+        at += n
+
+
 # ---- attention -----------------------------------------------------------------------
 
 def check_result(got, gl, want, want_lse, size, score, D):
