@@ -12,10 +12,11 @@
 // left), which carries 48 bits: FP64 adds run at about 2 a clock and SM here and
 // would set the time. FP64 takes over at the warps' sums, in one warp.
 // Bound: the chain of dependent loads, the cluster's two barriers and the
-// launch for few requests (one with eight rows of 248320: 10.2 us); the bytes of
-// one or two rows a request for many (64 requests at 157184: 19.8 us for 69 MB,
+// launch for few requests (one with eight rows of 248320: 10.0 us); the bytes of
+// one or two rows a request for many (64 requests at 157184: 19.7 us for 69 MB,
 // 3.5 TB/s: clusters that refused a draft read twice what the others do, and one
-// wave holds them all, so the mean SM is busy two thirds of the time).
+// wave holds them all, so the mean SM is busy two thirds of the time; 17.0 for 40
+// MB where the drafts were certain).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -48,7 +49,7 @@ struct VerifyParams {
   int vec;   // rows start on 16-byte boundaries
 };
 
-// hi + lo += w, w >= 0
+// hi + lo += w, w >= 0 (Knuth's two-sum: the rounded sum and its exact error)
 BWS_DEV void two_word_add(float& hi, float& lo, float w) {
   const float s = __fadd_rn(hi, w);
   const float b = __fsub_rn(s, hi);

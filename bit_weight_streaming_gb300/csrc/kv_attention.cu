@@ -30,11 +30,11 @@
 // reads without bank conflicts) and keeps its own m, l and O in registers; no
 // barrier joins them before the segment's end.
 // Bound: for few rows HBM and what a CTA spends at its start, a segment's end and
-// the join. One request of 131071 tokens, four kv heads of 256, one row: 52 us
-// for 268 MB (5.1 TB/s; 8 us of it start, end and join). 80 requests, 751 MB at
-// 128: 121 us (6.2 TB/s). 24 requests of five rows at 64, 141 MB: 36 us (3.9
-// TB/s), where half the cycles issue: a unit there is 2 KB against as many
-// instructions of softmax a token as at 256. Two CTAs an SM up to NT D = 128.
+// the join. One request of 131071 tokens, four kv heads of 256, one row: 50 us
+// for 268 MB (5.4 TB/s; 8 us of it start, end and join). 80 requests, 751 MB at
+// 128: 122 us (6.2 TB/s). 24 requests of five rows at 64, 141 MB: 37 us (3.8
+// TB/s), where neither memory nor issue is full: a unit there is 2 KB against as
+// many instructions of softmax a token as at 256, in one dependent chain a warp. Two CTAs an SM up to NT D = 128.
 // Copies of several boxes at once, and keys' and values' rings apart, lost 2 to
 // 18 us to fewer units in flight a warp. An unmarked L2 policy instead of
 // evict_first cost 21 us in the batch of 80.
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   auto slot_of = [&](int i) { return (first + i) * 2 + (i == 0 ? 1 : 0); };
   const int d4 = threadIdx.x % kLanes, at = threadIdx.x / kLanes;
   float top = kNone;
-  // a piece a lane: asked for one after the other by every thread they are a fifth of the join's time at 38 pieces
+  // a piece a lane: one after the other in every thread they cost 131071 tokens in 152 shares 3 us
   for (int i = threadIdx.x & 31; i < pieces; i += 32) top = fmaxf(top, p.part_ml[(size_t)slot_of(i) * kRows + n].x);
   top = warp_max(top);
   float4 a = make_float4(0, 0, 0, 0);
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
 // The kernel and its n8 tiles for a request's rows. A warp of attn_kernel holds
 // O for every dimension, NT * D <= 512; more rows of a wide head go to the other
 // kernel, up to 64 at a time (at 48 rows of 256 attn_kernel's three passes over
-// the cache took 112 us for 100001 tokens, the wide kernel 68); what is still
+// the cache took 112 us for 100001 tokens, the wide kernel 67); what is still
 // more goes in groups, each of which reads the cache again.
 struct Form {
   bool wide;

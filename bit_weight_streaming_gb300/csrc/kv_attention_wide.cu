@@ -26,7 +26,7 @@
 // margin, on which warps 0-7 vote, so most tiles exchange no maxima.
 // Bound: the chain of a tile, 4900 cycles at 48 rows of 256, of which the values'
 // mma.sync needs 3100 at 16 a quarter SM and HBM 2750: 100001 tokens of four kv
-// heads, 205 MB, take 68 us with the join (3.0 TB/s, 288 TFLOP/s). A segment costs
+// heads, 205 MB, take 67 us with the join (3.0 TB/s, 292 TFLOP/s). A segment costs
 // 8 to 10 us beside its tokens: its first tile passes every stage alone, through
 // code that is fetched anew.
 #include <atomic>

@@ -20,7 +20,7 @@ namespace {
 // for another. A row inside a block that this call takes reads it from the
 // free list, not from the table entry another CTA is writing.
 // Bound: launch and the chain of two dependent loads for few requests (one of
-// eight rows: 3.5 us); 384 requests with 374000 rows, 3.0 MB: 6.6 us, of which the
+// eight rows: 3.5 us); 384 requests with 374000 rows, 3.0 MB: 6.4 us, of which the
 // launch, the CTAs' own sums and the search of a row's request are all but half a
 // microsecond.
 
@@ -427,9 +427,10 @@ BWS_DEV void store_codes(uint8_t* p, const float (&x)[8], float inv) {
 // the issue slots waited for instructions (a 12382-row chunk: 128 us, and 162
 // with a CTA per run).
 // Bound: launch and three dependent loads for a decoded token (one: 3.8 us; 48
-// requests of five rows: 8.8 us, a serial run per warp). A 12382-row chunk at 64:
-// 55 us for 127 MB, 2.3 TB/s, by instructions: 54 % of the issue slots, the
-// conversions, norms and rotations of 38 million values.
+// requests of five rows: 8.9 us, a serial run per warp). A 12382-row chunk at 64:
+// 55 us for 127 MB, 2.3 TB/s: 20 % of DRAM and 52 % of the issue slots, so it is the
+// latency of loads and dependent instructions at 21 warps an SM, which 80 registers
+// and 64 KB of shared memory a CTA allow.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_constant__ AppendParams p) {
   using Hd = Head<D>;
