@@ -559,9 +559,11 @@ int bws_qk_norm_rope_append(const bws_qkv* in, const bws_kv_cache* cache,
  *   [n_requests]; out bf16 [n_rows][n_q_heads][head_dim]; lse fp32 [n_rows]
  *   [n_q_heads] (log of the sum of exponentials) or NULL. Device pointers; the
  *   lengths are read on the device, so a captured call follows them. Rows
- * before row_start[0] and from row_start[n_requests] on (row_start does not
- * decrease) belong to no request and give 0 (lse -inf). n_rows == 0 or
- * n_requests == 0 is a no-op.
+ *   before row_start[0] and from row_start[n_requests] on (row_start does not
+ *   decrease) belong to no request and give 0 (lse -inf). n_rows == 0 or
+ *   n_requests == 0 is a no-op.
+ * A prompt's rows are a request for every eight of them, each with the prompt's
+ * table row and kv_lens up to its last row.
  * 1 <= max_rows <= 8 bounds the rows of a request, n_q_heads / n_kv_heads in
  * 1..16. Of a request with more, the first max_rows are computed (their sight
  * goes by all n_r), the others give 0 (lse -inf) and the status word says so.

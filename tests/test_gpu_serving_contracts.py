@@ -107,6 +107,19 @@ def check_rows(q, c, table, start, kv, scale, out, lse, which):
     check_result(*(x[which] for x in (f64(out), f64(lse), want, want_lse, size, score)), q.shape[2])
 
 
+@pytest.mark.parametrize("D,H,K,first", [(64, 8, 2, 0), (128, 8, 2, 37), (256, 24, 4, 100)])
+def test_attention_prompt_in_eights(m, D, H, K, first):
+    """A prompt's 45 rows behind `first` cached tokens in one call: a request for every eight, over the same blocks."""
+    n, B = 45, 16
+    kv = first + n
+    c, q, t, _, _ = attention_case(m, D, H, K, B, [n], [kv], seed=first)
+    start = list(range(0, n, 8)) + [n]
+    lens = [first + e for e in start[1:]]
+    out, lse = m.kv_attention(q, c, ints(np.repeat(t, len(lens), 0)), ints(start), ints(lens), 8, lse=True)
+    torch.cuda.synchronize()
+    check_rows(q, c, t, [0, n], [kv], D ** -0.5, out, lse, slice(None))
+
+
 @pytest.mark.parametrize("D,H,K,n", [(64, 4, 2, 4), (128, 4, 2, 4), (256, 4, 1, 4), (256, 24, 4, 8), (128, 32, 2, 8)])
 @pytest.mark.parametrize("past", [1, 3, 9, 100, 2 ** 31 - 1])
 def test_attention_longer_than_its_table(m, D, H, K, n, past):
