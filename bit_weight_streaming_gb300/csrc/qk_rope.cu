@@ -5,8 +5,11 @@
 // forms the rows' angles once (qk_rotate.cuh); kAhead heads are asked for together.
 // rope_kernel holds both values of a pair in one lane, as two 8-byte loads, so that
 // nothing but the norm's sum passes between lanes, and takes the weights into the
-// angles: a pair costs six operations. Pairs (i, i + half) whose half is no multiple
-// of four go to rope_any_kernel, which brings them together in shared memory.
+// angles: a pair costs six operations. kAll: every dimension turns; otherwise a lane's
+// further dimensions pass through the same products, each without the other's (3001 rows
+// of 28 heads of 256, a quarter turning, 20.6 -> 21.9 us for the eight selects). Pairs
+// (i, i + half) whose half is no multiple of four go to rope_any_kernel, which brings them
+// together in shared memory.
 //
 // Bound: HBM, and the loads' latency at 24 warps an SM: 8191 rows of 32 + 8 heads of 128
 // in 30.7 us, 0.81 of the copy rate, 54 % of issue slots. (Pairs brought together by
@@ -57,7 +60,7 @@ struct Eight {
   uint2 a, b;
 };
 
-template <int D, bool kAdjacent>
+template <int D, bool kAdjacent, bool kAll>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
   using Hd = Head<D>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -77,13 +80,14 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   const int turned = half / 4;   // lanes that turn
   const int first = kAdjacent ? sl * 8 : sl < turned ? sl * 4 : in.rot + (sl - turned) * 8;
   const int gap = kAdjacent || sl >= turned ? 4 : half, second = first + gap;
+  const int turning = kAll ? 4 : half - sl * 4;   // of this lane's pairs
   float c[4], s[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     c[k] = 1.0f;
     s[k] = 0.0f;
   }
-  if (sl * 4 < half) {
+  if (turning > 0) {
     constexpr double kTurn = 0.15915494309189533577;      // 1 / 2 pi
     constexpr float kHi = (float)kTurn, kLo = (float)(kTurn - (double)kHi);
     int pos[4];
@@ -130,7 +134,22 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
       m[k / 2][1] = two(-wy[0] * s[k], -wy[1] * s[k + 1]);
       m[k / 2][2] = two(wx[0] * s[k], wx[1] * s[k + 1]);
       m[k / 2][3] = two(wy[0] * c[k], wy[1] * c[k + 1]);
+      if constexpr (!kAll) {
+        if (k >= turning) m[k / 2][1] = m[k / 2][2] = two(-0.0f, -0.0f);
+        else if (k + 1 >= turning) {
+          m[k / 2][1] = two(-wy[0] * s[k], -0.0f);
+          m[k / 2][2] = two(wx[0] * s[k], -0.0f);
+        }
+      }
     }
+    // What pairs k and k + 1 take of each other's value: of pairs that do not turn
+    // nothing, a zero, since 0 times an infinity or a NaN is NaN (and the factor is -0, so
+    // that a value of -0 stays one).
+    auto others = [&](Two v, int k) {
+      float lo, hi;
+      halves(v, lo, hi);
+      return two(k < turning ? lo : 0.0f, k + 1 < turning ? hi : 0.0f);
+    };
     const uint16_t* const here = src + first;
     uint16_t* const there = dst + first;
 #pragma unroll 1
@@ -173,8 +192,13 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float a0, a1, b0, b1;
-          halves(mul2(fma2(x[i], m[i][0], mul2(y[i], m[i][1])), r), a0, a1);
-          halves(mul2(fma2(y[i], m[i][3], mul2(x[i], m[i][2])), r), b0, b1);
+          Two xc = x[i], yc = y[i];
+          if constexpr (!kAll) {
+            xc = others(x[i], 2 * i);
+            yc = others(y[i], 2 * i);
+          }
+          halves(mul2(fma2(x[i], m[i][0], mul2(yc, m[i][1])), r), a0, a1);
+          halves(mul2(fma2(y[i], m[i][3], mul2(xc, m[i][2])), r), b0, b1);
           const __nv_bfloat162 p = kAdjacent ? __floats2bfloat162_rn(a0, b0) : __floats2bfloat162_rn(a0, a1);
           const __nv_bfloat162 q = kAdjacent ? __floats2bfloat162_rn(a1, b1) : __floats2bfloat162_rn(b0, b1);
           o[kAdjacent ? 2 * i : i] = *reinterpret_cast<const uint32_t*>(&p);
@@ -316,8 +340,10 @@ extern "C" int bws_qk_norm_rope(const bws_qk* in, uint16_t* q_out, uint16_t* k_o
   cudaStream_t st = as_stream(stream);
   auto launch = [&](auto d) {
     constexpr int kD = decltype(d)::value;
-    if (in->interleaved) return launch_pdl(rope_kernel<kD, true>, grid, kRopeThreads, 0, st, p);
-    if (in->rot / 2 % 4 == 0) return launch_pdl(rope_kernel<kD, false>, grid, kRopeThreads, 0, st, p);
+    if (in->interleaved && in->rot == kD) return launch_pdl(rope_kernel<kD, true, true>, grid, kRopeThreads, 0, st, p);
+    if (in->interleaved) return launch_pdl(rope_kernel<kD, true, false>, grid, kRopeThreads, 0, st, p);
+    if (in->rot == kD) return launch_pdl(rope_kernel<kD, false, true>, grid, kRopeThreads, 0, st, p);
+    if (in->rot / 2 % 4 == 0) return launch_pdl(rope_kernel<kD, false, false>, grid, kRopeThreads, 0, st, p);
     return launch_pdl(rope_any_kernel<kD>, grid, kRopeThreads, 2 * kRopeWarps * 256 * 4, st, p);
   };
   const cudaError_t e = D == 64 ? launch(std::integral_constant<int, 64>()) : D == 128 ? launch(std::integral_constant<int, 128>())
