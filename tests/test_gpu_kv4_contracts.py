@@ -1,11 +1,12 @@
 """The 4-bit cache's entry points on the GPU at the edges of their contracts: dimensions that do not turn beside ones that
-are not finite."""
+are not finite, infinite queries."""
 import numpy as np
 import pytest
 import torch
 
 from gpu_util import bws, device, f64, np_
 from oracle import serving as S
+from test_gpu_kv4 import case4, check4, check_long
 from test_gpu_serving import freqs, gen, ints, rows
 
 pytestmark = pytest.mark.gpu
@@ -72,3 +73,40 @@ def test_rope_unturned_dimensions_under_the_norm(m, D, rot, inter):
             if t % 3:
                 h = t % x.shape[1]
                 assert np.isnan(y[t, h]).sum() == 1 and (np.delete(y[t, h], rot + t) == 0).all()
+
+
+# ---- attention: queries that are not finite -------------------------------------------------
+
+@pytest.mark.parametrize("D,H,K,n,kv,wide", [
+    (64, 4, 2, 1, 1, 0), (64, 4, 2, 2, 2, 0), (128, 4, 2, 1, 1, 0), (128, 40, 8, 5, 5, 0), (256, 6, 1, 1, 2, 0), (256, 24, 4, 8, 8, 0),
+    (256, 24, 4, 1, 1, 4000), (128, 8, 2, 1, 2, 3000), (64, 8, 8, 2, 2, 200000), (256, 24, 4, 1, 1, 200000), (256, 24, 4, 8, 8, 200000),
+    (128, 40, 8, 8, 8, 200000)])
+def test_attention4_infinite_queries(m, D, H, K, n, kv, wide):
+    """A query row with an infinity has no score that is a number, so its result and log-sum-exp are NaN, of one or two
+    tokens too, whose keys may all be of the other sign there; in whole segments, clusters, on the line and of many rows (by
+    tables of `wide` tokens). Other rows keep their results."""
+    c, q, t, s, mx = case4(m, D, H, K, 16, [n], [kv], seed=D + n)
+    t = np.pad(t, ((0, 0), (0, max(wide // 16 - t.shape[1], 0))), constant_values=-1)
+    c.k[..., D // 4] = 0x11 if D == 64 else 0x99       # no zero code: 0.5 or -0.5 everywhere, in dimensions D / 2 and the next
+    many = (D, n * H // K) in ((256, 48), (128, 40)) and wide
+    (check_long if many else check4)(m, c, q, t, s, [kv], mx)
+    bad = np.zeros((n, H), dtype=bool)
+    for i, (j, h, x) in enumerate([(0, 0, "inf"), (0, H - 1, "-inf"), (n - 1, H // 2, "inf"), (n - 1, 1, "-inf")]):
+        q[j, h, D // 2 + i % 2] = float(x)
+        bad[j, h] = True
+    out, lse = m.kv4_attention(q, c, ints(t), ints(s), ints([kv]), mx, lse=True)
+    torch.cuda.synchronize()
+    assert np.array_equal(np_(torch.isnan(out).all(-1)), bad) and np.array_equal(np_(torch.isnan(out).any(-1)), bad)
+    assert np.array_equal(np_(torch.isnan(lse)), bad)
+    if not many:
+        check4(m, c, q, t, s, [kv], mx)
+
+
+def test_attention4_infinite_query_without_tokens(m):
+    """A row that sees no token gives zero whatever its query holds."""
+    c, q, t, s, mx = case4(m, 128, 4, 2, 16, [3], [1], seed=3)
+    q[0] = float("inf")
+    q[1, 0, 0] = float("nan")
+    out, lse = m.kv4_attention(q, c, ints(t), ints(s), ints([1]), mx, lse=True)
+    torch.cuda.synchronize()
+    assert (out[:2] == 0).all() and (lse[:2] == -float("inf")).all() and torch.isfinite(out[2]).all()
