@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
     sc_n = scales_of(ids);
   };
   // The query rows to f16, each scaled by a power of two. `slot`: the NaN mask to clear.
+  // A row that holds an infinity is all NaN: its scores are none, but of keys of one sign
+  // there they would all be -infinity, which is what tokens that a row does not see get.
   auto store_queries = [&](int slot) {
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
@@ -202,17 +204,20 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT>::kCtas) attn_kernel
       __half2* dst = reinterpret_cast<__half2*>(T.q + n * S::kQStride);
       float x[D / 32];
       float top = 0.0f;
+      bool bad = false;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         x[i] = __uint_as_float(i % 2 ? qx[k][i / 2] & 0xFFFF0000u : qx[k][i / 2] << 16);
         if (fabsf(x[i]) < INFINITY) top = fmaxf(top, fabsf(x[i]));
+        else bad = true;
       }
+      bad = __any_sync(0xffffffffu, bad);
       top = warp_max(top);
       const int e = top > 0.0f ? min(max(floor_log2_abs(top), -100), 126) : 0;
       const float f = exp2i(-e);
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) dst[lane + 32 * i] = __floats2half2_rn(x[2 * i] * f, x[2 * i + 1] * f);
-      if (lane == 0) T.q_scale[n] = p.scale * kLog2e * exp2i(e);
+      if (lane == 0) T.q_scale[n] = bad ? NAN : p.scale * kLog2e * exp2i(e);
     }
     for (int i = tid; i < D; i += kAttnThreads) T.nan_mask[slot][i] = 0;
   };

@@ -546,7 +546,8 @@ int bws_qk_norm_rope_append(const bws_qkv* in, const bws_kv_cache* cache,
  * over tokens t <= kv_lens[r] - n_r + j for row j of request r's n_r =
  * row_start[r+1] - row_start[r] rows (so the rows are the request's last
  * tokens, already in the cache). Query head h reads kv head h / (n_q_heads /
- * n_kv_heads). A row that sees no token gives 0 (lse -inf). Codes are exact in
+ * n_kv_heads). A row that sees no token gives 0 (lse -inf), another whose query
+ * holds an infinity or a NaN gives NaN. Codes are exact in
  * the products; sums and softmax statistics are FP32. A weight (times its
  * block's value scale) is rounded to f16 for the values' product: by 2^-11
  * down to 2^-23 of the row's largest, by at most 2^-34 of that largest below.

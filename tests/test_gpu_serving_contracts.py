@@ -6,8 +6,8 @@ import torch
 
 from gpu_util import bws, device, f64, np_
 from oracle import formats as F, serving as S
-from test_gpu_serving import attention_case, check_append, check_plan, check_verify, freqs, gen, held, ints, make_cache, \
-    rows, verify_case
+from test_gpu_serving import attention_case, check_append, check_attention, check_plan, check_verify, freqs, gen, held, \
+    ints, make_cache, rows, verify_case
 
 pytestmark = pytest.mark.gpu
 
@@ -270,6 +270,21 @@ def test_attention_dominant_token(m, D, H, K, n, gap):
     out, lse = m.kv_attention(q, c, ints(t), ints([0, n]), ints([kv]), n, 1.0, lse=True)
     torch.cuda.synchronize()
     check_result(f64(out), f64(lse), *want, D)
+
+
+@pytest.mark.parametrize("D,H,K,n,kv", [(64, 4, 2, 1, 1), (64, 4, 2, 2, 2), (128, 4, 2, 1, 1), (128, 8, 2, 2, 2),
+                                        (128, 40, 8, 5, 5), (256, 6, 1, 1, 2), (256, 24, 4, 8, 8), (256, 24, 4, 2, 600)])
+def test_attention_infinite_queries(m, D, H, K, n, kv):
+    """A query row with an infinity has no score that is a number: NaN, of one or two tokens too, whose keys may all be of
+    the other sign there. Other rows keep their results."""
+    c, q, t, s, mx = attention_case(m, D, H, K, 16, [n], [kv], seed=D + n)
+    c.k[..., D // 2] = 0x38                             # 1
+    check_attention(m, c, q, t, s, [kv], mx)
+    bad = np.zeros((n, H), dtype=bool)
+    for j, h, x in ((0, 0, "inf"), (0, H - 1, "-inf"), (n - 1, H // 2, "inf"), (n - 1, 1, "-inf")):
+        q[j, h, D // 2], bad[j, h] = float(x), True
+    out, lse = check_attention(m, c, q, t, s, [kv], mx)
+    assert np.array_equal(np_(torch.isnan(out).all(-1)), bad) and np.array_equal(np_(torch.isnan(lse)), bad)
 
 
 # ---- arguments -------------------------------------------------------------------------
