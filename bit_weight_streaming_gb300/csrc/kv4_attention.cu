@@ -944,10 +944,10 @@ int wide_tiles_for(int D, int rows) {
 
 // A segment's start costs the wide kernel 6 us (queries to planes), so it has work of
 // some length only, by the tables' width: a table's tokens times dimensions, and these
-// times tables and heads. us, wide and not: 8 rows of 6 heads of 256 over 100001 tokens 51
-// and 97, over 20000 27 and 30, over 6000 22 and 19; 40 such requests of 6000 78 and 101,
-// of 2000 47 and 50, of 777 41 and 37; 40 rows of 128 over 100001 66 and 118, 30000 31 and
-// 45, 6000 20 and 20, 40 such requests of 2000 55 and 61.
+// times tables and heads. us, wide and not: 8 rows of 6 heads of 256 over 100001 tokens 55
+// and 97, over 20000 28 and 30, over 6000 22 and 19; 40 such requests of 6000 81 and 101,
+// of 2000 50 and 50, of 777 41 and 37; 40 rows of 128 over 100001 68 and 118, 30000 33 and
+// 45, 6000 20 and 20, 40 such requests of 2000 58 and 61.
 constexpr long long kWideTable = 1 << 18, kWideWork = 1 << 24;
 
 size_t workspace_of(int D, int rows) {

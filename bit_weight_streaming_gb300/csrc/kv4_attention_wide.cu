@@ -21,15 +21,19 @@
 // ahead of the weights of the tile before; two copy, keys with their scales and values.
 // mbarriers with bounded waits join them; a wait that runs out marks the result and goes on.
 //
-// Bound: a tile's chain. 8 rows of 6 heads over 100001 tokens take 51.3 us, 20.7 tiles a
-// CTA of some 2900 cycles each: scores to weights 2000 of them, the values' conversion
-// 2100 beside, both products 2300 if shared memory gave 128 bytes a cycle (it feeds
-// every operand); the start (queries to planes) 10,000, the end 5,000. Two planes instead
-// of six would save 3 us, a quarter of the conversion 4. Steps: a thread's keys' scales
-// to TMEM and fourteen warps 98 -> 69, copies and scales by two warps of their own 64,
-// six planes and O rescaled beside the weights' warps 63, a tile's values in two parts
-// 55, ten binades of room 51.6. Of 128 dimensions (8 rows of 5 heads, 8 kv heads, as long)
-// 65.6 us: keys' scales copied, not read a tile ahead, and larger boxes 66.6 -> 65.6.
+// Bound: a tile's chain. 8 rows of 6 heads over 100001 tokens take 55.0 us, 20.7 tiles a
+// CTA of some 3300 cycles each: scores to weights all of them (of it 490 for new maxima
+// and 680 of waits for the sum, which waits while O is rescaled), the values' conversion
+// 2200 beside and 840 more where O is rescaled, both products 2300 if shared memory gave
+// 128 bytes a cycle (it feeds every operand); the start (queries to planes) 10,000, the end
+// 5,000. Two planes instead of six would save 3 us, a quarter of the conversion 4. Steps:
+// a thread's keys' scales to TMEM and fourteen warps 98 -> 69, copies and scales by two
+// warps of their own 64, six planes and O rescaled beside the weights' warps 63, a tile's
+// values in two parts 55. Of 128 dimensions (8 rows of 5 heads, 8 kv heads, as long) 67.7
+// us: keys' scales copied, not read a tile ahead, and larger boxes save one.
+// Room above a row's maximum is the other kernels' (kMargin). Ten binades instead of six
+// take 51.3 us for 55.0, but f16's least step is then 2^-29 of a row's largest weight:
+// tokens 28 octaves behind one that carries no value gave a result 29 % off.
 #include <atomic>
 
 #include "copy_ring.h"
@@ -47,11 +51,6 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = kWide4Tile;
 constexpr int kPlanes = 6, kPairs = kPlanes / 2;
 constexpr int kBarSoft = 1, kBarWork = 3;   // named barriers of warps 0-3, 4-7 (kBarSoft + 1) and 0-11
-// Room above a row's maximum. Wider than the other kernel's: a maximum that passes it
-// has O rescaled between two tiles' products (some 2400 cycles of the sum's pipeline), and
-// a weight is rounded by half of f16's least step, 2^-25, under a largest of 2^5 or more.
-// (8 rows of 6 heads over 100001 tokens: 6 binades 55.5 us, 9 52.8, 12 50.6, 20 49.5.)
-constexpr float kWideMargin = 10.0f;
 constexpr float kLeastScale = 1.0f / 512.0f;   // of E4M3
 // Polls of a wait, each of which sleeps 10 us at most: without that time given the
 // waiting warps took a quarter of the issue slots.
@@ -531,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn4_wide_kernel(const __grid_co
         float x[kHalf];
         uint32_t a[kHalf], b[kHalf];
         // (all asked for at once where the registers allow it: at 256 dimensions that spills
-        // and takes 52.6 us for 51.3, at 128 it saves two of 67.6)
+        // and takes 1.3 us more of the 55, at 128 it saves two of 70)
         auto ask = [&](int n) {
           tmem_load8(s_at + n, a + n);
           tmem_load8(s_at + R + n, b + n);
@@ -579,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn4_wide_kernel(const __grid_co
             if (lane < kHalf) {
               const bool first = ((fresh >> lane) & 1u) != 0u;
               float up = -INFINITY;
-              for (int w = 0; w < kQuads; ++w) up = fmaxf(up, T.top[w][row] - (kTop - kWideMargin));
+              for (int w = 0; w < kQuads; ++w) up = fmaxf(up, T.top[w][row] - (kTop - kMargin));
               still = first && up == -INFINITY;
               if (!first || still) up = fmaxf(up, 0.0f);
               moves = up != 0.0f;

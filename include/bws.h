@@ -667,8 +667,7 @@ int bws_kv4_read(const bws_kv4_cache* cache, const int32_t* block_table, int max
  * is off by up to 2^-25 of that. With more than 16 rows a kv head at 256 dimensions, or
  * more than 32 at 128, over tables that hold 2^18 / head_dim tokens or more and, times
  * requests and kv heads, 2^24 / head_dim or more, both products run on the tensor cores of the fifth
- * generation: there a weight is rounded by 2^-11 down to 2^-19 and by at most 2^-30
- * below, and a query's value is off by up to 2^-14.9 of the largest of its 16
+ * generation: there a query's value is off by up to 2^-14.9 of the largest of its 16
  * dimensions (its own BF16 step is 2^-9 of itself) or 2^-21 of the row's.
  * One kernel, or two. A request's results do not depend on the others' content, but
  * their order of summation goes by the whole call's lengths.

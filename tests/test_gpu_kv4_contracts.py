@@ -1,12 +1,12 @@
 """The 4-bit cache's entry points on the GPU at the edges of their contracts: dimensions that do not turn beside ones that
-are not finite, infinite queries."""
+are not finite, infinite queries, tokens far apart in weight."""
 import numpy as np
 import pytest
 import torch
 
 from gpu_util import bws, device, f64, np_
 from oracle import serving as S
-from test_gpu_kv4 import case4, check4, check_long
+from test_gpu_kv4 import case4, check4, check_long, long_table, make_cache4
 from test_gpu_serving import freqs, gen, ints, rows
 
 pytestmark = pytest.mark.gpu
@@ -110,3 +110,27 @@ def test_attention4_infinite_query_without_tokens(m):
     out, lse = m.kv4_attention(q, c, ints(t), ints(s), ints([1]), mx, lse=True)
     torch.cuda.synchronize()
     assert (out[:2] == 0).all() and (lse[:2] == -float("inf")).all() and torch.isfinite(out[2]).all()
+
+
+# ---- attention: many rows a kv head --------------------------------------------------------
+
+@pytest.mark.parametrize("D,H,K,n", [(256, 24, 4, 3), (256, 24, 4, 8), (128, 40, 8, 8), (64, 8, 4, 4), (128, 8, 4, 2)])
+def test_attention4_tail_behind_a_dominant_token(m, D, H, K, n):
+    """A first token without a value, 23 to 30 octaves above some hundred others that are all alike, so that their weights'
+    roundings add up: held to half of f16's least step under a largest weight of 2^9, 2^-34 of it a token, by tables for
+    either kernel. (A query of one dimension has one score for all of these tokens, so that its own rounding is no part.)"""
+    R, B, tokens = 160 // K, 16, 600
+    t = np.random.RandomState(D).permutation(R * 38).reshape(R, 38)
+    c = make_cache4(m, R * 38, K, B, D)
+    c.k.zero_()
+    c.k_scale.fill_(0x38)                    # 1
+    c.v.fill_(0x22)                          # 1, 1
+    c.v_scale.fill_(0x38)
+    first = torch.tensor(t[:, 0].tolist(), device=device())
+    c.k[first, :, 0, 4] = 0x07               # 6 in dimension 8
+    c.k_scale[first, :, 0, 0] = 0x48         # 4
+    c.v_scale[first, :, 0] = 0
+    q = torch.zeros((R * n, H, D), dtype=torch.bfloat16, device=device())
+    q[..., 8] = 1 + torch.arange(R * n, device=device())[:, None] % 9 / 32 + torch.arange(H, device=device()) % 4 / 64
+    start = np.arange(R + 1) * n
+    check4(m, c, q, long_table(t, K, B, D), start, [tokens] * R, n, scale=23 * np.log(2.0) / 24)
