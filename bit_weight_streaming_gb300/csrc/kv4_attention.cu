@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "device_counts.h"
 #include "kv4_attention.cuh"
 #include "kv4_cache.cuh"
 #include "kv_cache.cuh"
@@ -896,28 +897,26 @@ cudaError_t launch_attn4(const Attn4Params& p, cudaStream_t st) {
 
 template <int D, int NT, bool kMany>
 int clusters_of(int ctas) {
-  static std::atomic<int> known[kMaxSpread + 1];   // and one
-  int n = known[ctas].load(std::memory_order_relaxed);
-  if (n > 0) return n - 1;
-  static std::atomic<unsigned long long> attr{0};
-  if (set_smem_once(attr, attn4_kernel<D, NT, kMany>, attn4_smem<D, NT, kMany>()) != cudaSuccess) return 0;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(Shape4<D, NT, kMany>::kThreads);
-  cfg.dynamicSmemBytes = attn4_smem<D, NT, kMany>();
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim.x = (unsigned)ctas;
-  a[0].val.clusterDim.y = 1;
-  a[0].val.clusterDim.z = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, attn4_kernel<D, NT, kMany>, &cfg) != cudaSuccess) {
+  static DeviceCounts<kMaxDevices, kMaxSpread + 1> counts;
+  return counts.get(current_device(), ctas, [&]() {
+    static std::atomic<unsigned long long> attr{0};
+    if (set_smem_once(attr, attn4_kernel<D, NT, kMany>, attn4_smem<D, NT, kMany>()) != cudaSuccess) return -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(Shape4<D, NT, kMany>::kThreads);
+    cfg.dynamicSmemBytes = attn4_smem<D, NT, kMany>();
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = (unsigned)ctas;
+    a[0].val.clusterDim.y = 1;
+    a[0].val.clusterDim.z = 1;
+    cfg.attrs = a;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, attn4_kernel<D, NT, kMany>, &cfg) == cudaSuccess) return n;
     cudaGetLastError();
-    n = 0;
-  }
-  known[ctas].store(n + 1, std::memory_order_relaxed);
-  return n;
+    return -1;
+  });
 }
 
 template <int D, int NT, bool kMany>

@@ -1,6 +1,8 @@
 """The 4-bit cache's entry points on the CPU: their refusals, and the oracle's pieces against hand-worked values (no
 GPU)."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -160,3 +162,33 @@ def test_read4_by_hand():
     v = np.arange(2 * 16).reshape(2, 1, 16, 1) + 1.0
     out = S.read4(v, np.array([[1, -1], [0, 1]]), [15, 14], [1, 3, 7], 8)
     assert out[:, 0, 0].tolist() == [0, 32, 0, 15, 16, 17, 18, 0]
+
+
+COUNTS_MODEL = r"""
+#include <cstdio>
+#include "device_counts.h"
+static bws::DeviceCounts<4, 9> counts;
+int main() {
+  int bad = 0, asked = 0;
+  auto ask = [&](int n) { return [&asked, n]() { ++asked; return n; }; };
+  bad += counts.get(0, 8, ask(18)) != 18 || asked != 1;
+  bad += counts.get(0, 8, ask(5)) != 18 || asked != 1;    // known
+  bad += counts.get(1, 8, ask(7)) != 7 || asked != 2;     // another device's own
+  bad += counts.get(0, 4, ask(36)) != 36 || asked != 3;   // another index
+  bad += counts.get(0, 8, ask(5)) != 18 || counts.get(1, 8, ask(5)) != 7 || asked != 3;
+  bad += counts.get(3, 2, ask(-1)) != 0 || asked != 4;    // failed: none, and asked again
+  bad += counts.get(3, 2, ask(0)) != 0 || asked != 5;
+  bad += counts.get(3, 2, ask(9)) != 0 || asked != 5;     // none is an answer too
+  std::printf("%d\n", bad);
+  return bad != 0;
+}
+"""
+
+
+def test_counts_are_each_devices_own(tmp_path):
+    """How many clusters run at once is asked for on every device, and again where the question failed."""
+    src = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_weight_streaming_gb300", "csrc")
+    (tmp_path / "counts.cpp").write_text(COUNTS_MODEL)
+    subprocess.run(["g++", "-std=c++17", "-I", src, "-o", str(tmp_path / "counts"), str(tmp_path / "counts.cpp")], check=True)
+    r = subprocess.run([str(tmp_path / "counts")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
