@@ -88,6 +88,17 @@ def _row_stride(name, t):
     return t.stride(0)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _on(device, f, *args):
+    """f(*args) with the CUDA device of index `device` current."""
+    if _current_device() == device:
+        return f(*args)
+    with torch.cuda.device(device):
+        return f(*args)
+
+
 def _fail(rc, what):
     if rc:
         check(rc, what)
@@ -244,7 +255,7 @@ def kv_attention(q, cache, block_table, row_start, kv_lens, max_rows, scale=None
     so = lib()
     size = cache._attn_ws.get((H, max_rows))
     if size is None:
-        size = cache._attn_ws[H, max_rows] = kv_attention_workspace_size(H, cache.kv_heads, D, max_rows)
+        size = cache._attn_ws[H, max_rows] = _on(q.get_device(), kv_attention_workspace_size, H, cache.kv_heads, D, max_rows)
     buf = _ws(ws, size, q.device)
     if not buf.is_cuda or buf.dtype is not _U8:
         raise BwsError(f"the workspace must be CUDA uint8 memory; it is {buf.dtype} on {buf.device}")
@@ -257,16 +268,9 @@ def kv_attention(q, cache, block_table, row_start, kv_lens, max_rows, scale=None
 
 # ---- the 4-bit cache ---------------------------------------------------------------
 
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
 def _call(what, device, f, *args):
     """f(*args, stream) on the tensors' device, whichever is current."""
-    if _current_device() == device:
-        rc = f(*args, _raw_stream(device))
-    else:
-        with torch.cuda.device(device):
-            rc = f(*args, _raw_stream(device))
+    rc = _on(device, f, *args, _raw_stream(device))
     if rc:
         check(rc, what)
 
@@ -470,7 +474,7 @@ def kv4_attention(q, cache, block_table, row_start, kv_lens, max_rows, scale=Non
     so = lib()
     size = cache._attn_ws.get((H, max_rows))
     if size is None:
-        size = cache._attn_ws[H, max_rows] = kv4_attention_workspace_size(H, cache.kv_heads, D, max_rows)
+        size = cache._attn_ws[H, max_rows] = _on(device, kv4_attention_workspace_size, H, cache.kv_heads, D, max_rows)
     buf = _ws(ws, size, q.device)
     if buf.dtype is not _U8 or buf.get_device() != device:
         raise BwsError(f"the workspace must be uint8 memory on cuda:{device}; it is {buf.dtype} on {buf.device}")

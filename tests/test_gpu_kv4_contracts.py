@@ -1,5 +1,5 @@
 """The 4-bit cache's entry points on the GPU at the edges of their contracts: dimensions that do not turn beside ones that
-are not finite, infinite queries, tokens far apart in weight."""
+are not finite, infinite queries, tokens far apart in weight, other devices."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +7,7 @@ import torch
 from gpu_util import bws, device, f64, np_
 from oracle import serving as S
 from test_gpu_kv4 import case4, check4, check_long, long_table, make_cache4
-from test_gpu_serving import freqs, gen, ints, rows
+from test_gpu_serving import attention_case, freqs, gen, ints, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,34 @@ def test_attention4_tail_behind_a_dominant_token(m, D, H, K, n):
     q[..., 8] = 1 + torch.arange(R * n, device=device())[:, None] % 9 / 32 + torch.arange(H, device=device()) % 4 / 64
     start = np.arange(R + 1) * n
     check4(m, c, q, long_table(t, K, B, D), start, [tokens] * R, n, scale=23 * np.log(2.0) / 24)
+
+
+# ---- devices -------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_workspace_size_of_the_tensors_device(m, monkeypatch, bits):
+    """The size that a handle keeps is that of its tensors' device, whichever is current at the first call."""
+    from bit_weight_streaming_gb300 import serving
+    if bits == 4:
+        c, q, t, s, n = case4(m, 64, 4, 2, 16, [1], [20], seed=6)
+    else:
+        c, q, t, s, n = attention_case(m, 64, 4, 2, 16, [1], [20], seed=6)
+    name, entered, asked = "kv4_attention_workspace_size" if bits == 4 else "kv_attention_workspace_size", [], []
+    size = getattr(serving, name)
+
+    class Guard(torch.cuda.device):
+        def __enter__(self):
+            entered.append(self.idx)
+            return super().__enter__()
+
+        def __exit__(self, *a):
+            entered.pop()
+            return super().__exit__(*a)
+
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(serving, "_current_device", lambda: q.get_device() + 1, raising=False)
+    monkeypatch.setattr(serving, name, lambda *a: asked.append(list(entered)) or size(*a))
+    f = m.kv4_attention if bits == 4 else m.kv_attention
+    out = [f(q, c, ints(t), ints(s), ints([20]), n) for _ in range(2)]
+    torch.cuda.synchronize()
+    assert asked == [[q.get_device()]] and torch.equal(*out)
