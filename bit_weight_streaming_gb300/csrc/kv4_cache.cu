@@ -28,13 +28,14 @@ BWS_DEV Kv4Side side_of(const bws_kv4_cache& c, int side) {
 //
 // A thread takes 16 values, which share a scale: their largest magnitude is an
 // integer maximum of BF16 patterns (a NaN is above infinity's, and becomes the
-// scale's NaN), then two divisions, a reciprocal and sixteen products, each an
-// IEEE operation, so that the codes can be formed again bit for bit. A warp takes
-// one head of the rows whose codes are 256 bytes and whose scales are one sector.
+// scale's NaN), then a sixth of it, a division by the head's number where it has one, a
+// reciprocal and sixteen products, each rounded as IEEE's operation is, so that the codes
+// can be formed again bit for bit. A warp takes one head of the rows whose codes are 256
+// bytes and whose scales are one sector.
 //
 // Bound: the latency of a round's loads at 41 warps an SM (65 % of issue slots). Long
 // writes take two rounds a warp, both asked for at once (12382 rows of 16 heads of 64:
-// 13.7 us, 0.70 of the copy rate; one round 14.3, four 14.8, eight 19.2); 134 rows of 8
+// 13.6 us, 0.70 of the copy rate; one round 14.3, four 14.8, eight 19.2); 134 rows of 8
 // heads of 128, 1.8 us, are a launch and two dependent loads.
 
 struct Append4Params {
@@ -104,11 +105,7 @@ __global__ void __launch_bounds__(kThreads) append4_kernel(const __grid_constant
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
     top = max(top & 0xFFFFu, top >> 16);
-    // (the largest over 6: a product and Markstein's correction by its remainder, the
-    // quotient's rounding for each of BF16's 128 significands)
-    constexpr float kSixth = 1.0f / 6.0f;
-    const float a0 = __uint_as_float(top << 16), y0 = __fmul_rn(a0, kSixth);
-    const float sixth = top < 0x7F80u ? __fmaf_rn(__fmaf_rn(-6.0f, y0, a0), kSixth, y0) : a0;
+    const float a0 = __uint_as_float(top << 16), sixth = top < 0x7F80u ? sixth_of(a0) : a0;
     const float need = g == 1.0f ? sixth : __fdiv_rn(sixth, g);
     const uint32_t code = f32x2_to_e4m3x2(0.0f, need) & 0xFFu;
     const float d = __fmul_rn(e4m3_to_f32(code), g);

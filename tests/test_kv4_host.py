@@ -2,6 +2,7 @@
 GPU)."""
 import ctypes
 import os
+import shutil
 import subprocess
 
 import numpy as np
@@ -191,4 +192,37 @@ def test_counts_are_each_devices_own(tmp_path):
     (tmp_path / "counts.cpp").write_text(COUNTS_MODEL)
     subprocess.run(["g++", "-std=c++17", "-I", src, "-o", str(tmp_path / "counts"), str(tmp_path / "counts.cpp")], check=True)
     r = subprocess.run([str(tmp_path / "counts")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+
+
+SIXTH_MODEL = r"""
+#include <cstdio>
+#include <cstdint>
+#include <cstring>
+#include "kv4_cache.cuh"
+int main() {
+  int bad = 0;
+  for (uint32_t b = 0; b < 0x7F80u; ++b) {   // every finite BF16 magnitude
+    const uint32_t w = b << 16;
+    float a;
+    std::memcpy(&a, &w, 4);
+    bad += bws::sixth_of(a) != a / 6.0f;
+  }
+  std::printf("%d\n", bad);
+  return bad != 0;
+}
+"""
+
+
+def test_sixth_is_the_quotients_rounding(tmp_path):
+    """The write's product in place of a division by 6 gives the quotient's FP32 rounding of every BF16 magnitude."""
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("nvcc not found")
+    src = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_weight_streaming_gb300", "csrc")
+    (tmp_path / "sixth.cu").write_text(SIXTH_MODEL)
+    r = subprocess.run([nvcc, "-std=c++17", "-O2", "-I", src, "-o", str(tmp_path / "sixth"), str(tmp_path / "sixth.cu")],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
+    r = subprocess.run([str(tmp_path / "sixth")], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
