@@ -1,12 +1,13 @@
 """The 4-bit cache's entry points on the GPU at the edges of their contracts: dimensions that do not turn beside ones that
-are not finite, infinite queries, tokens far apart in weight, other devices."""
+are not finite, infinite queries, tokens far apart in weight, truncated requests of many rows, prompts in eights, other
+devices."""
 import numpy as np
 import pytest
 import torch
 
 from gpu_util import bws, device, f64, np_
 from oracle import serving as S
-from test_gpu_kv4 import case4, check4, check_long, long_table, make_cache4
+from test_gpu_kv4 import case4, check4, check_long, check_result, check_rope, long_table, make_cache4, sides
 from test_gpu_serving import attention_case, freqs, gen, ints, rows
 
 pytestmark = pytest.mark.gpu
@@ -75,6 +76,21 @@ def test_rope_unturned_dimensions_under_the_norm(m, D, rot, inter):
                 assert np.isnan(y[t, h]).sum() == 1 and (np.delete(y[t, h], rot + t) == 0).all()
 
 
+@pytest.mark.parametrize("D,rot,n,H,K", [(64, 20, 5, 3, 1), (64, 62, 70, 5, 2), (64, 36, 3001, 24, 8), (128, 28, 2000, 32, 8),
+                                         (256, 100, 900, 24, 4)])
+def test_rope_pairs_off_whole_lanes(m, D, rot, n, H, K):
+    """Halves that are no multiple of four: 64 dimensions, many heads a warp, in place, far positions."""
+    g = gen(D + rot)
+    w = 1 + 0.2 * torch.randn(D, generator=g, device=device())
+    pos = np.stack([np.arange(n) - 3, 2 ** 24 - 2 + np.arange(n), np.random.RandomState(n).randint(-2 ** 31, 2 ** 31, n)])
+    axis = np.arange(rot // 2) % 3
+    q, k = rows(n, H, D, g), rows(n, K, D, g)
+    a = check_rope(m, q, k, pos, freqs(rot), axis, w, None)
+    b = m.qk_norm_rope(q, k, ints(pos), freqs(rot), ints(axis), w, None, q_out=q, k_out=k)
+    torch.cuda.synchronize()
+    assert b[0] is q and torch.equal(q, a[0]) and torch.equal(k, a[1])
+
+
 # ---- attention: queries that are not finite -------------------------------------------------
 
 @pytest.mark.parametrize("D,H,K,n,kv,wide", [
@@ -134,6 +150,44 @@ def test_attention4_tail_behind_a_dominant_token(m, D, H, K, n):
     q[..., 8] = 1 + torch.arange(R * n, device=device())[:, None] % 9 / 32 + torch.arange(H, device=device()) % 4 / 64
     start = np.arange(R + 1) * n
     check4(m, c, q, long_table(t, K, B, D), start, [tokens] * R, n, scale=23 * np.log(2.0) / 24)
+
+
+@pytest.mark.parametrize("D,H,K", [(128, 16, 2), (256, 24, 4), (128, 40, 8)])
+def test_attention4_long_table_truncated_requests(m, D, H, K):
+    """More rows than max_rows: the first of them within the bound of every output, each with the sight that it has by all
+    of its request's rows (check_long's bound, but for weights held to 2^-34 of the largest)."""
+    kv, rw, mx = [200, 90, 350], [2, 8, 1], 5
+    c, q, t, s, _ = case4(m, D, H, K, 16, rw, kv, seed=32)
+    wide = long_table(t, K, 16, D)
+    ws = m.Workspace()
+    out, lse = m.kv4_attention(q, c, ints(wide), ints(s), ints(kv), mx, lse=True, ws=ws)
+    torch.cuda.synchronize()
+    assert m.status_word(ws) == 0x10
+    assert (out[2 + mx:10] == 0).all() and (lse[2 + mx:10] == -float("inf")).all()
+    live = [0, 1, *range(2, 2 + mx), 10]
+    cut_s, cut_kv = [0, 2, 2 + mx, 3 + mx], [200, 90 - (8 - mx), 350]     # the same sight
+    x, (k, v) = f64(q[live]), sides(c)
+    most = np.abs(x).reshape(*x.shape[:2], D // 16, 16).max(-1)
+    off = 2.0 ** -14.9 * np.repeat(most, 16, -1) + 2.0 ** -21 * most.max(-1)[..., None]
+    ref, ref_lse, (size, score, total) = S.attention4(x, k, v, wide, cut_s, cut_kv, D ** -0.5)
+    planes = S.attention4(off, np.abs(k), v, wide, cut_s, cut_kv, D ** -0.5)[2][1]
+    check_result(f64(out[live]), f64(lse[live]), ref, ref_lse, size, score + planes * 2.0 ** 24 / D, total, D)
+
+
+@pytest.mark.parametrize("D,H,K,first,wide", [(64, 8, 4, 0, 0), (128, 8, 2, 300, 0), (256, 24, 4, 0, 0), (256, 24, 4, 700, 0),
+                                              (256, 24, 4, 700, 1), (128, 40, 8, 130, 1), (128, 40, 8, 0, 0)])
+def test_attention4_prompt_in_eights(m, D, H, K, first, wide):
+    """A prompt's 45 rows behind `first` cached tokens in one call: a request for every eight, over the same blocks; by
+    tables for either kernel."""
+    n, B = 45, 16
+    c, q, t, _, _ = case4(m, D, H, K, B, [n], [first + n], seed=first + 1)
+    start = [*range(0, n, 8), n]
+    lens = [first + e for e in start[1:]]
+    t = np.repeat(t, len(lens), 0)
+    if wide:
+        check_long(m, c, q, t, start, lens, 8)
+    else:
+        check4(m, c, q, t, start, lens, 8)
 
 
 # ---- devices -------------------------------------------------------------------------------
