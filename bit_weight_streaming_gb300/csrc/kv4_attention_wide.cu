@@ -33,7 +33,7 @@
 // us: keys' scales copied, not read a tile ahead, and larger boxes save one.
 // Room above a row's maximum is the other kernels' (kMargin). Ten binades instead of six
 // take 51.3 us for 55.0, but f16's least step is then 2^-29 of a row's largest weight:
-// tokens 28 octaves behind one that carries no value gave a result 29 % off.
+// tokens 28.5 octaves behind one that carries no value gave a result 29 % off.
 #include <atomic>
 
 #include "copy_ring.h"

@@ -1,7 +1,8 @@
 // Shared by the attention kernels over the 8-bit cache (kv_attention.cu for few
 // query rows, kv_attention_wide.cu for many) and over the 4-bit one
-// (kv4_attention.cu): their parameters, the line of shares, the join of partial
-// results, the shared-memory tiles.
+// (kv4_attention.cu, kv4_attention_wide.cu): their parameters, the line of shares, the
+// rows without a result, the shared-memory tiles. Each cache joins its partial results by
+// a kernel of its own.
 #pragma once
 #include <cuda.h>
 
